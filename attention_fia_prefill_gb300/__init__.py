@@ -8,11 +8,20 @@ block-sparse attention behind a C ABI (include/fia.h), with this thin binding.
     fia_decode(query, key, value, ...)   -> (attention_out, softmax_lse)
     bsa_forward(query, key, value, block_sparse_mask, block_shape, ...)
 
+Paged serving, with lengths in device memory:
+
+    fia_block_table_append(context_lens, new_lens, free_blocks, block_table, ...)
+                                         -> (slot_mapping, kv_lens, cu_new_lens, num_blocks)
+    fia_cache_write(key, value, key_cache, value_cache, slot_mapping)
+    fia_decode_window(query, key, value, actual_seq_kvlen=..., pre_tokens=..., sink_tokens=..., ...)
+
 The library must have been built (attention_fia_prefill_gb300.build.build());
 there is no CPU path.
 """
 from ._binding import (FIAError, INT32_MAX, bsa_forward, fia_decode, fia_device_status, fia_prefill,  # noqa: F401
                        fia_prefill_mla, fia_prefill_paged, load_library)
+from ._paged import fia_block_table_append, fia_cache_write, fia_decode_window  # noqa: F401
 
-__all__ = ["fia_prefill", "fia_prefill_mla", "fia_prefill_paged", "fia_decode", "bsa_forward", "fia_device_status", "FIAError",
+__all__ = ["fia_block_table_append", "fia_cache_write", "fia_decode_window",
+           "fia_prefill", "fia_prefill_mla", "fia_prefill_paged", "fia_decode", "bsa_forward", "fia_device_status", "FIAError",
            "load_library"]

@@ -30,7 +30,7 @@ EXPORTS = [
     "fia_decode", "bsa_get_workspace_size", "bsa_forward", "bsa_fp8_get_workspace_size", "bsa_forward_fp8",
     "fia_device_status", "fia_status_string",
     "fia_last_error", "fia_profile_next_call", "fia_debug_set_wait_limit_ns", "fia_debug_set_decode_path", "fia_decode_no_alloc",
-    "fia_debug_plan_decode",
+    "fia_debug_plan_decode", "fia_block_table_append", "fia_cache_write", "fia_decode_window",
 ]
 
 
@@ -118,6 +118,14 @@ def load_library(path: str | None = None):
     lib.fia_debug_plan_decode.argtypes = [i32p, ctypes.c_int, ctypes.c_int, ctypes.c_int, i32p, ctypes.c_int, i32p,
                                           ctypes.c_int, i32p, ctypes.c_int, ip, ip]
     lib.fia_debug_plan_decode.restype = st
+    # the paged-serving operators (_paged.py) pass packed descriptors as byte strings
+    d, i64 = ctypes.c_char_p, ctypes.c_int64
+    lib.fia_block_table_append.argtypes = [d, d, d, i64, d, d, d, d, d, vp]
+    lib.fia_block_table_append.restype = st
+    lib.fia_cache_write.argtypes = [d, i64, d, i64, d, d, d, vp]
+    lib.fia_cache_write.restype = st
+    lib.fia_decode_window.argtypes = [d, d, d, d, d, P, i64, d, d, vp]
+    lib.fia_decode_window.restype = st
     if path is None:
         _lib = lib
     return lib

@@ -14,10 +14,12 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "internal.h"
 
 using namespace fia;
 
+namespace fia {
 namespace {
 
 thread_local std::string g_last_error;
@@ -26,18 +28,12 @@ thread_local std::string g_last_error;
 // call on this thread (fia_profile_next_call).
 thread_local cudaEvent_t g_prof_start = nullptr, g_prof_stop = nullptr;
 
-template <typename F>
-cudaError_t profiled(cudaStream_t s, F&& launch) {
-  cudaEvent_t a = g_prof_start, b = g_prof_stop;
+}  // namespace
+
+void take_profile_events(cudaEvent_t* start, cudaEvent_t* stop) {
+  *start = g_prof_start;
+  *stop = g_prof_stop;
   g_prof_start = g_prof_stop = nullptr;
-  if (a != nullptr) {
-    cudaError_t e = cudaEventRecord(a, s);
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t e = launch();
-  if (e != cudaSuccess) return e;
-  if (b != nullptr) return cudaEventRecord(b, s);
-  return cudaSuccess;
 }
 
 fia_status fail(fia_status s, const char* fmt, ...) {
@@ -50,8 +46,9 @@ fia_status fail(fia_status s, const char* fmt, ...) {
   return s;
 }
 
+namespace {
+
 constexpr int64_t kInt32Max = 2147483647;
-constexpr size_t kHeader = 256;   // workspace bytes [0, 256): device status word + padding
 
 // Every call gets a fresh epoch; kernels tag the workspace's status word (and
 // the decode kernel its per-unit counters) with it, so nothing in a reused
@@ -64,6 +61,8 @@ unsigned long long next_epoch() { return g_epoch.fetch_add(1, std::memory_order_
 std::atomic<unsigned long long> g_wait_limit_ns{0};
 // fia_debug_set_decode_path: 1 runs the tcgen05 decode kernel for every unit
 std::atomic<int> g_decode_force_tc{0};
+
+}  // namespace
 
 // A call's device status: the word at the start of its workspace, a fresh
 // epoch, and the wait limit.
@@ -89,14 +88,6 @@ bool present(const fia_tensor* t) { return t != nullptr && t->data != nullptr &&
 bool given(const fia_tensor* t) {
   return t != nullptr && t->ndim > 0 && (t->data != nullptr || numel(t) == 0);
 }
-
-bool is_half(int32_t dt) { return dt == FIA_DTYPE_F16 || dt == FIA_DTYPE_BF16; }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-enum Layout { L_BSH, L_BSND, L_BNSD, L_TND, L_BAD };
 
 Layout parse_layout(const char* s) {
   if (s == nullptr) return L_BSH;
@@ -129,14 +120,14 @@ EncodeTiledFn encode_fn() {
 // rank-d tiled map of 16-bit elements, 128-byte swizzle, box {64, box_rows, 1, ...}
 // Boxes of 128 bytes x box_rows: 64 16-bit elements, or 128 8-bit ones (u8).
 fia_status make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-                    uint32_t box_rows, bool u8 = false) {
+                    uint32_t box_rows, bool u8, const uint32_t* box_dims) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return fail(FIA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (no CUDA driver?)");
   cuuint64_t gd[5], gs[4];
   cuuint32_t box[5], es[5];
   for (int i = 0; i < rank; ++i) {
     gd[i] = dims[i];
-    box[i] = i == 0 ? (u8 ? 128 : 64) : (i == 1 ? box_rows : 1);
+    box[i] = box_dims != nullptr ? box_dims[i] : i == 0 ? (u8 ? 128 : 64) : (i == 1 ? box_rows : 1);
     es[i] = 1;
   }
   for (int i = 0; i + 1 < rank; ++i) gs[i] = strides_bytes[i];
@@ -201,7 +192,7 @@ fia_status resolve_tnd(const int64_t* lst, int64_t n, int64_t T, std::vector<int
 
 // GQA rules (num_key_value_heads): Q_N a multiple of KV_N, Q_N / KV_N <= 64.
 // The MLA case (query_rope/key_rope given) takes Q_N up to 128 over KV_N = 1.
-fia_status resolve_heads(const fia_params* p, int64_t& N1, int64_t& N2, int64_t max_ratio = 64) {
+fia_status resolve_heads(const fia_params* p, int64_t& N1, int64_t& N2, int64_t max_ratio) {
   N1 = p->num_heads;
   N2 = p->num_key_value_heads == 0 ? p->num_heads : p->num_key_value_heads;
   if (N1 <= 0 || N2 <= 0) return fail(FIA_ERR_HEADS, "num_heads=%lld num_key_value_heads=%lld", (long long)N1, (long long)N2);
@@ -564,7 +555,7 @@ fia_status check_ws(void* ws, size_t have, size_t need) {
 
 // Encode the (D, S, N, B) maps of a dense tensor (TND: (D, T, N, 1)).
 fia_status dense_map(CUtensorMap* m, const fia_tensor* t, Layout L, int64_t B, int64_t N, int64_t S, int64_t D,
-                     bool u8 = false) {
+                     bool u8) {
   uint64_t dims[4], st[3];
   const uint64_t e = u8 ? 1 : 2;
   if (L == L_BNSD) {
@@ -796,9 +787,6 @@ fia_status clear_status(void* ws, cudaStream_t stream) {
   return cuda_check(cudaMemsetAsync(ws, 0, 8, stream), "status reset");
 }
 
-}  // namespace
-
-namespace fia {
 void set_last_error(int status, const char* message) {
   fail(static_cast<fia_status>(status), "%s", message);
 }

@@ -1,0 +1,262 @@
+// Host side of the paged-serving entry points (include/fia.h): argument
+// validation and launches.  Lengths stay on the device; nothing here waits for
+// the GPU or copies to it.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "host.h"
+#include "paged.h"
+
+using namespace fia;
+
+namespace {
+
+constexpr int64_t kMaxKeys = int64_t(1) << 30;     // keys of one sequence (tile arithmetic stays in 32 bits)
+constexpr int64_t kMaxInt = 2147483647;
+
+// An int32 vector on the device; n < 0: any length.
+fia_status check_i32(const fia_tensor* t, int64_t n, const char* name) {
+  if (!given(t)) return fail(FIA_ERR_NULL, "%s is required", name);
+  if (t->dtype != FIA_DTYPE_I32) return fail(FIA_ERR_DTYPE, "%s must be int32", name);
+  if (t->ndim != 1) return fail(FIA_ERR_SHAPE, "%s must be 1-D", name);
+  if (n >= 0 && t->shape[0] != n)
+    return fail(FIA_ERR_SHAPE, "%s has %lld entries, expected %lld", name, (long long)t->shape[0], (long long)n);
+  if (t->shape[0] > kMaxInt) return fail(FIA_ERR_SHAPE, "%s has more than 2^31-1 entries", name);
+  if (reinterpret_cast<uintptr_t>(t->data) % 4 != 0) return fail(FIA_ERR_ALIGNMENT, "%s not 4-byte aligned", name);
+  return FIA_OK;
+}
+
+bool overlap(const fia_tensor* a, const fia_tensor* b) {   // int32 tensors
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a->data), b0 = reinterpret_cast<uintptr_t>(b->data);
+  const uintptr_t na = uintptr_t(numel(a)) * 4, nb = uintptr_t(numel(b)) * 4;
+  return na > 0 && nb > 0 && a0 < b0 + nb && b0 < a0 + na;
+}
+
+#define FIA_TRY(x)                        \
+  do {                                    \
+    const fia_status st_ = (x);           \
+    if (st_ != FIA_OK) return st_;        \
+  } while (0)
+
+int elem_bytes(int32_t dt) { return dt == FIA_DTYPE_F8E4M3 ? 1 : 2; }
+
+// One tensor of fia_cache_write and its pool -> entry y of the launch.
+fia_status write_side(const fia_tensor* x, int64_t stride, const fia_tensor* cache, int64_t T, int64_t nblk, int64_t bs,
+                      int y, CacheWriteParams& p, const char* name) {
+  if (!is_half(x->dtype) && x->dtype != FIA_DTYPE_F8E4M3)
+    return fail(FIA_ERR_DTYPE, "%s must be f16, bf16 or e4m3", name);
+  if (cache->dtype != x->dtype) return fail(FIA_ERR_DTYPE, "%s and its cache differ in type", name);
+  if (x->ndim != 3) return fail(FIA_ERR_SHAPE, "%s must be (T, KV_N, D)", name);
+  if (x->shape[0] != T) return fail(FIA_ERR_SHAPE, "%s has %lld tokens, slot_mapping %lld", name, (long long)x->shape[0], (long long)T);
+  const int64_t e = elem_bytes(x->dtype), N = x->shape[1], D = x->shape[2];
+  if (N <= 0 || D <= 0 || N > kMaxInt / 16 || D > kMaxInt / 16 || N * D * e > kMaxInt)
+    return fail(FIA_ERR_SHAPE, "%s: KV_N %lld, D %lld", name, (long long)N, (long long)D);
+  if (D * e % 16 != 0) return fail(FIA_ERR_UNSUPPORTED, "%s: rows of a head must be a multiple of 16 bytes", name);
+  if (stride == 0) stride = N * D;
+  if (stride < 0 || (T > 1 && stride < N * D) || stride * e % 16 != 0)
+    return fail(FIA_ERR_ALIGNMENT, "%s: token stride %lld (at least %lld elements, a multiple of 16 bytes)", name,
+                (long long)stride, (long long)(N * D));
+  const bool bnbd = cache->ndim == 4;
+  if (bnbd ? (cache->shape[0] != nblk || cache->shape[1] != N || cache->shape[2] != bs || cache->shape[3] != D)
+           : (cache->ndim != 3 || cache->shape[0] != nblk || cache->shape[1] != bs || cache->shape[2] != N * D))
+    return fail(FIA_ERR_SHAPE, "%s's cache must be (%lld, KV_N, %lld, D) or (%lld, %lld, KV_N*D) for its heads", name,
+                (long long)nblk, (long long)bs, (long long)nblk, (long long)bs);
+  if (!aligned16(x->data) || !aligned16(cache->data)) return fail(FIA_ERR_ALIGNMENT, "%s or its cache not 16-byte aligned", name);
+  p.src[y] = static_cast<const uint8_t*>(x->data);
+  p.dst[y] = static_cast<uint8_t*>(cache->data);
+  p.src_row[y] = stride * e;
+  p.dst_blk[y] = N * bs * D * e;
+  p.dst_row[y] = (bnbd ? D : N * D) * e;
+  p.dst_head[y] = (bnbd ? bs * D : D) * e;
+  p.vecs[y] = int(N * D * e / 16);
+  p.head_vecs[y] = int(D * e / 16);
+  return FIA_OK;
+}
+
+// Query, cache, length and output arguments shared by the decode entry points.
+fia_status span_params(const fia_tensor* q, const fia_tensor* k, const fia_tensor* v, const fia_tensor* table,
+                       const fia_tensor* kvlen, const fia_params* prm, const fia_tensor* out, const fia_tensor* lse,
+                       SpanParams& p, int64_t& D) {
+  memset(&p, 0, sizeof(p));
+  if (prm == nullptr) return fail(FIA_ERR_NULL, "params is NULL");
+  if (!given(q) || !given(k) || !given(v) || !given(out))
+    return fail(FIA_ERR_NULL, "query/key/value/attention_out required");
+  const Layout L = parse_layout(prm->input_layout);
+  if (L == L_BAD) return fail(FIA_ERR_LAYOUT, "input_layout '%s' not supported", prm->input_layout);
+  if (L == L_TND) return fail(FIA_ERR_UNSUPPORTED, "TND decode is not implemented");
+  if (!is_half(q->dtype) || k->dtype != q->dtype || v->dtype != q->dtype || out->dtype != q->dtype)
+    return fail(FIA_ERR_DTYPE, "query/key/value/attention_out must share fp16 or bf16");
+  if (prm->actual_seq_qlen != nullptr || prm->actual_seq_kvlen != nullptr)
+    return fail(FIA_ERR_SEQLEN, "lengths are a device tensor here: params' actual_seq lists must be NULL");
+  int64_t N1, N2, B, S;
+  FIA_TRY(resolve_heads(prm, N1, N2));
+  if (!same_shape(q, out)) return fail(FIA_ERR_SHAPE, "attention_out must have the query's shape");
+  FIA_TRY(dense_dims(q, L, N1, B, S, D, "query"));
+  if (S < 1 || S > 16) return fail(FIA_ERR_UNSUPPORTED, "decode takes Q_S in 1..16 (got %lld)", (long long)S);
+  if (D != 64 && D != 128) return fail(FIA_ERR_UNSUPPORTED, "decode head dim %lld (kernels take 64 or 128)", (long long)D);
+  if (N1 / N2 * S > 64)
+    return fail(FIA_ERR_UNSUPPORTED, "decode rows per KV head (Q_N / KV_N x Q_S = %lld) above 64", (long long)(N1 / N2 * S));
+  if (!(prm->scale_value > 0.0) || !std::isfinite(prm->scale_value))
+    return fail(FIA_ERR_UNSUPPORTED, "scale_value must be finite and > 0");
+  if (!same_shape(k, v)) return fail(FIA_ERR_SHAPE, "key and value shapes differ");
+  if (!aligned16(q->data) || !aligned16(k->data) || !aligned16(v->data) || !aligned16(out->data))
+    return fail(FIA_ERR_ALIGNMENT, "query/key/value/attention_out must be 16-byte aligned");
+  if (B * N2 > kMaxInt / 16) return fail(FIA_ERR_SHAPE, "B x KV_N = %lld is too large", (long long)(B * N2));
+  int64_t S2;
+  if (present(table)) {
+    if (table->dtype != FIA_DTYPE_I32 || table->ndim != 2 || table->shape[0] != B)
+      return fail(FIA_ERR_BLOCK_TABLE, "block_table must be int32 (B, maxBlocksPerSeq)");
+    if (reinterpret_cast<uintptr_t>(table->data) % 4 != 0) return fail(FIA_ERR_ALIGNMENT, "block_table not 4-byte aligned");
+    const int64_t bs = prm->block_size;
+    if (bs <= 0 || bs % 16 != 0 || bs > kMaxKeys)
+      return fail(FIA_ERR_BLOCK_TABLE, "block_size %lld: a multiple of 16", (long long)bs);
+    const bool bnbd = k->ndim == 4;
+    if (bnbd ? (k->shape[1] != N2 || k->shape[2] != bs || k->shape[3] != D)
+             : (k->ndim != 3 || k->shape[1] != bs || k->shape[2] != N2 * D))
+      return fail(FIA_ERR_SHAPE, "paged key must be (blocknum, KV_N, block_size, D) or (blocknum, block_size, KV_N*D)");
+    if (k->shape[0] > kMaxInt) return fail(FIA_ERR_SHAPE, "more than 2^31-1 blocks");
+    if (!present(kvlen)) return fail(FIA_ERR_SEQLEN, "page attention needs actual_seq_kvlen");
+    S2 = table->shape[1] > kMaxKeys / bs ? kMaxKeys + 1 : table->shape[1] * bs;
+    p.block_table = static_cast<const int32_t*>(table->data);
+    p.table_stride = table->shape[1];
+    p.block_size = int(bs);
+    p.n_blocks = int(k->shape[0]);
+    p.blk_stride = N2 * bs * D;
+    p.head_stride = bnbd ? bs * D : D;
+    p.row_stride = bnbd ? D : N2 * D;
+  } else {
+    if (table != nullptr && table->ndim > 0 && B > 0) {
+      // a table without columns: no sequence has a key
+      return fail(FIA_ERR_BLOCK_TABLE, "block_table has no entries");
+    }
+    int64_t Bk, Dk;
+    FIA_TRY(dense_dims(k, L, N2, Bk, S2, Dk, "key"));
+    if (Bk != B || Dk != D) return fail(FIA_ERR_SHAPE, "key must be (B, ..., D) like the query");
+    int64_t st[3];
+    bns_strides(L, N2, S2, D, st);
+    p.blk_stride = st[0];
+    p.head_stride = st[1];
+    p.row_stride = st[2];
+    p.n_blocks = int(std::min<int64_t>(B, kMaxInt));
+    p.block_size = 16;   // not read
+  }
+  if (S2 > kMaxKeys) return fail(FIA_ERR_SHAPE, "more than 2^30 keys per sequence");
+  if (kvlen != nullptr && kvlen->ndim > 0) {
+    FIA_TRY(check_i32(kvlen, B, "actual_seq_kvlen"));
+    p.kv_len = static_cast<const int32_t*>(kvlen->data);
+  }
+  FIA_TRY(check_lse(lse, prm, L, B, N1, S, 0));
+  int64_t qs[3];
+  bns_strides(L, N1, S, D, qs);
+  p.q = q->data;
+  p.out = out->data;
+  p.q_sb = qs[0]; p.q_sn = qs[1]; p.q_ss = qs[2];
+  if (prm->softmax_lse_flag != 0) p.lse = static_cast<float*>(lse->data);
+  p.lse_sb = N1 * S; p.lse_sn = S; p.lse_ss = 1;
+  p.k = k->data;
+  p.v = v->data;
+  p.kv_max = int(S2);
+  p.B = int(B); p.N1 = int(N1); p.N2 = int(N2);
+  p.group = int(N1 / N2);
+  p.q_tokens = int(S);
+  p.rows = int(N1 / N2 * S);
+  p.pre = int(std::min<int64_t>(std::max<int64_t>(prm->pre_tokens, 0), kMaxInt));
+  p.scale_log2 = float(prm->scale_value * 1.4426950408889634);
+  return FIA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fia_status fia_block_table_append(const fia_tensor* context_lens, const fia_tensor* new_lens,
+                                  const fia_tensor* free_blocks, int64_t block_size, const fia_tensor* block_table,
+                                  const fia_tensor* slot_mapping, const fia_tensor* kv_lens,
+                                  const fia_tensor* cu_new_lens, const fia_tensor* num_blocks, void* stream) {
+  FIA_TRY(check_i32(context_lens, -1, "context_lens"));
+  const int64_t B = context_lens->shape[0];
+  FIA_TRY(check_i32(new_lens, B, "new_lens"));
+  FIA_TRY(check_i32(free_blocks, -1, "free_blocks"));
+  FIA_TRY(check_i32(slot_mapping, -1, "slot_mapping"));
+  FIA_TRY(check_i32(kv_lens, B, "kv_lens"));
+  FIA_TRY(check_i32(cu_new_lens, B, "cu_new_lens"));
+  FIA_TRY(check_i32(num_blocks, 1, "num_blocks"));
+  if (!given(block_table)) return fail(FIA_ERR_NULL, "block_table is required");
+  if (block_table->dtype != FIA_DTYPE_I32) return fail(FIA_ERR_DTYPE, "block_table must be int32");
+  if (block_table->ndim != 2 || block_table->shape[0] != B || block_table->shape[1] > kMaxInt)
+    return fail(FIA_ERR_BLOCK_TABLE, "block_table must be (B, columns)");
+  if (reinterpret_cast<uintptr_t>(block_table->data) % 4 != 0)
+    return fail(FIA_ERR_ALIGNMENT, "block_table not 4-byte aligned");
+  if (block_size < 1 || block_size > kMaxInt) return fail(FIA_ERR_BLOCK_TABLE, "block_size %lld", (long long)block_size);
+  const fia_tensor* ins[] = {context_lens, new_lens, free_blocks};
+  const fia_tensor* outs[] = {block_table, slot_mapping, kv_lens, cu_new_lens, num_blocks};
+  for (int i = 0; i < 5; ++i) {
+    for (const fia_tensor* t : ins)
+      if (overlap(outs[i], t)) return fail(FIA_ERR_UNSUPPORTED, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return fail(FIA_ERR_UNSUPPORTED, "two outputs overlap");
+  }
+  TableParams p;
+  memset(&p, 0, sizeof(p));
+  p.context_lens = static_cast<const int32_t*>(context_lens->data);
+  p.new_lens = static_cast<const int32_t*>(new_lens->data);
+  p.free_blocks = static_cast<const int32_t*>(free_blocks->data);
+  p.block_table = static_cast<int32_t*>(block_table->data);
+  p.slot_mapping = static_cast<int32_t*>(slot_mapping->data);
+  p.kv_lens = static_cast<int32_t*>(kv_lens->data);
+  p.cu_new_lens = static_cast<int32_t*>(cu_new_lens->data);
+  p.num_blocks = static_cast<int32_t*>(num_blocks->data);
+  p.B = int(B);
+  p.n_free = int(free_blocks->shape[0]);
+  p.table_cols = int(block_table->shape[1]);
+  p.n_tokens = int(slot_mapping->shape[0]);
+  p.block_size = int(block_size);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_check(profiled(s, [&] { return launch_block_table(p, s); }), "block table launch");
+}
+
+fia_status fia_cache_write(const fia_tensor* key, int64_t key_token_stride, const fia_tensor* value,
+                           int64_t value_token_stride, const fia_tensor* key_cache, const fia_tensor* value_cache,
+                           const fia_tensor* slot_mapping, void* stream) {
+  if (!given(key) || !given(key_cache)) return fail(FIA_ERR_NULL, "key and key_cache are required");
+  const bool two = value != nullptr && value->ndim > 0;
+  if (two != (value_cache != nullptr && value_cache->ndim > 0))
+    return fail(FIA_ERR_NULL, "value and value_cache must be given together");
+  if (two && (!given(value) || !given(value_cache))) return fail(FIA_ERR_NULL, "value or value_cache has no data");
+  FIA_TRY(check_i32(slot_mapping, -1, "slot_mapping"));
+  const int64_t T = slot_mapping->shape[0];
+  if (key_cache->ndim != 3 && key_cache->ndim != 4) return fail(FIA_ERR_SHAPE, "key_cache must be 3-D or 4-D");
+  const int64_t nblk = key_cache->shape[0], bs = key_cache->ndim == 4 ? key_cache->shape[2] : key_cache->shape[1];
+  if (bs < 1 || bs > kMaxInt) return fail(FIA_ERR_BLOCK_TABLE, "block_size %lld", (long long)bs);
+  CacheWriteParams p;
+  memset(&p, 0, sizeof(p));
+  FIA_TRY(write_side(key, key_token_stride, key_cache, T, nblk, bs, 0, p, "key"));
+  if (two) FIA_TRY(write_side(value, value_token_stride, value_cache, T, nblk, bs, 1, p, "value"));
+  if (T == 0 || nblk == 0) return FIA_OK;
+  p.slots = static_cast<const int32_t*>(slot_mapping->data);
+  p.n_slots = nblk > kMaxInt / bs ? kMaxInt : nblk * bs;
+  p.n_tokens = int(T);
+  p.block_size = int(bs);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_check(profiled(s, [&] { return launch_cache_write(p, s); }), "cache write launch");
+}
+
+fia_status fia_decode_window(const fia_tensor* query, const fia_tensor* key, const fia_tensor* value,
+                             const fia_tensor* block_table, const fia_tensor* actual_seq_kvlen,
+                             const fia_params* params, int64_t sink_tokens, const fia_tensor* attention_out,
+                             const fia_tensor* softmax_lse, void* stream) {
+  if (query != nullptr && query->ndim > 0 && numel(query) == 0) return FIA_OK;   // empty query
+  SpanParams p;
+  int64_t D;
+  FIA_TRY(span_params(query, key, value, block_table, actual_seq_kvlen, params, attention_out, softmax_lse, p, D));
+  if (params->pre_tokens < 0) return fail(FIA_ERR_UNSUPPORTED, "pre_tokens must be 0 or more");
+  if (sink_tokens < 0) return fail(FIA_ERR_UNSUPPORTED, "sink_tokens must be 0 or more");
+  p.sink = int(std::min<int64_t>(sink_tokens, p.kv_max));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_check(
+      profiled(s, [&] { return launch_span_decode(p, int(D), query->dtype == FIA_DTYPE_BF16, sm_count(), s); }),
+      "window decode launch");
+}
+
+}  // extern "C"

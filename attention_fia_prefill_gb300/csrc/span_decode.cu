@@ -1,0 +1,462 @@
+// Decode over the visible span of each sequence: a sliding window and sink
+// tokens (fia_decode_window), or the keys behind a shared prefix joined with
+// the prefix's partial results (fia_decode_shared_prefix).
+//
+//   token i of a sequence's Q_S new tokens sits at position p = L - Q_S + i and
+//   sees key j when j <= p and (p - j <= pre or j < sink); j >= base only;
+//   out = softmax(scale q K^T) V over the keys it sees, lse = log sum exp.
+//
+// Lengths are read on the device, so the grid depends on sizes alone and a
+// captured call follows new lengths.  A unit is (batch, kv head), its rows the
+// g heads x Q_S tokens (at most 64).  Its keys are the 16-key tiles of the
+// sinks and of [first row's window, L): a list whose length the device knows.
+//   * Work: a cluster of 1..8 CTAs runs a unit, each CTA four warps.  A warp
+//     owns 16 rows (mma.sync m16n8k16); units of up to 16 rows give each warp
+//     keys of its own (tile v of the list belongs to group v mod groups), those
+//     of 32 / 64 rows pair / quadruple the warps of a group over the same tiles.
+//   * Data: a group streams its tiles through a ring of its own with cp.async
+//     (16-byte pieces, XOR-swizzled so that ldmatrix has no bank conflicts): no
+//     barrier across groups in the loop.  A tile lies in one page (16 divides
+//     the page size); page ids come 32 at a time, one per lane, a batch ahead.
+//     Keys that no row sees are not read: they are zero-filled (a freed page
+//     behind the window may hold anything, and 0 * NaN would reach the sums).
+//   * Softmax: running maximum and sum per row and group in fp32, scores in
+//     log2 units; P is rounded to the cache's type for the tensor cores (half
+//     a step, relative, of each weight), its sum is not rounded.
+//   * Join: the groups' (O, max, sum) meet in shared memory, the CTAs' over
+//     distributed shared memory, with the exact weights 2^(m - max m): one
+//     launch, no workspace, no atomics, the same bits on every run.
+#include <algorithm>
+#include <type_traits>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace fia {
+namespace {
+
+constexpr int kSpanThreads = 128;
+constexpr int kSpanTile = 16;        // keys of a tile
+
+template <int D, int MT>
+struct SpanCfg {
+  static constexpr int kGroups = 4 / MT;
+  static constexpr int kStages = 3 * MT;                  // per group: the same bytes in flight for every MT
+  static constexpr int kTileBytes = kSpanTile * D * 2;    // K or V
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kRing = kGroups * kStages * kStageBytes;
+  // after the loop: O of every group [kGroups][16 MT][D] and (max, sum)
+  static constexpr int kOffML = kGroups * 16 * MT * D * 4;
+  static constexpr int kMerge = kOffML + kGroups * 16 * MT * 8;
+  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 128;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// d += A B, one m16n8k16 tile, fp32 accumulators
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t smem, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// The weight of a partial result with maximum m in a sum with maximum top
+// (an empty one, m = -inf, has none).
+__device__ __forceinline__ float join_weight(float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); }
+
+template <int D, bool BF16, int MT>
+__global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __grid_constant__ SpanParams p) {
+  using C = SpanCfg<D, MT>;
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int CH = D / 8;                       // 16-byte pieces of a row
+  constexpr int KK = D / 16;                      // k-steps of Q K^T
+  constexpr int NT = D / 8;                       // n-tiles of O
+  constexpr int ST = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rt = warp % MT, kg = warp / MT;
+  const int fg = lane >> 2, ft = lane & 3;
+  const uint32_t cs = cluster_size(), rank = cluster_rank();
+  const int unit = blockIdx.x / cs;
+  const int b = unit / p.N2, kvh = unit - b * p.N2;
+
+  grid_dep_launch();
+  grid_dep_wait();
+
+  const int L = p.kv_len == nullptr ? p.kv_max : min(max(p.kv_len[b], 0), p.kv_max);
+  const int first = L - p.q_tokens;               // position of token 0 (may be negative: tokens that see nothing)
+  // the tiles that hold a key some row may see: the sinks' [base / 16, t_sink)
+  // and [t_win, t_end)
+  const int t_end = (L + kSpanTile - 1) / kSpanTile;
+  const int t_base = p.base / kSpanTile;
+  const int t_sink = min(t_end, max(t_base, (p.sink + kSpanTile - 1) / kSpanTile));
+  const int64_t win = int64_t(first) - p.pre;     // first key of token 0's window
+  const int t_win = max(t_sink, int(max(win, int64_t(0)) / kSpanTile));
+  const int n_sink = max(0, t_sink - t_base);
+  const int n_tiles = n_sink + max(0, t_end - t_win);
+  const int groups = int(cs) * C::kGroups;
+  const int gi = int(rank) * C::kGroups + kg;
+  const int n = n_tiles > gi ? (n_tiles - gi + groups - 1) / groups : 0;
+  auto tile_key = [&](int i) -> int {             // first key of the group's i-th tile
+    const int v = gi + i * groups;
+    return (v < n_sink ? t_base + v : t_win + v - n_sink) * kSpanTile;
+  };
+
+  // ---------------------------------------------------------------- loads
+  auto page_of = [&](int i) -> int {              // block id of the group's i-th tile; -1: none
+    if (i >= n) return -1;
+    if (p.block_table == nullptr) return b;
+    const int id = p.block_table[int64_t(b) * p.table_stride + tile_key(i) / p.block_size];
+    return id >= 0 && id < p.n_blocks ? id : -1;
+  };
+  int ids = page_of(lane), ids_next = page_of(32 + lane), ids_blk = 0;
+  const uint32_t ring = smem_u32(smem) + kg * ST * C::kStageBytes;
+  const T* kp = static_cast<const T*>(p.k) + kvh * p.head_stride;
+  const T* vp = static_cast<const T*>(p.v) + kvh * p.head_stride;
+  auto issue = [&](int i) {
+    if ((i >> 5) != ids_blk) {
+      ids = ids_next;
+      ++ids_blk;
+      ids_next = page_of(((ids_blk + 1) << 5) + lane);
+    }
+    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+    if (i < n) {
+      const int j0 = tile_key(i);
+      const int in_page = p.block_table == nullptr ? j0 : j0 % p.block_size;
+      const uint32_t st = ring + (i % ST) * C::kStageBytes;
+      const int64_t off0 = int64_t(max(id, 0)) * p.blk_stride + int64_t(in_page) * p.row_stride;
+#pragma unroll
+      for (int it = 0; it < kSpanTile * CH / (32 * MT); ++it) {
+        const int idx = it * 32 * MT + rt * 32 + lane;
+        const int row = idx / CH, c = idx % CH;
+        const int j = j0 + row;
+        const bool live = id >= 0 && j < L && j >= p.base && (j < p.sink || j >= win);
+        const uint32_t dst = st + row * (D * 2) + ((c ^ (row & 7)) << 4);
+        const int64_t off = live ? off0 + int64_t(row) * p.row_stride + c * 8 : 0;
+        cp_async_zfill<16>(dst, kp + off, live ? 16u : 0u);
+        cp_async_zfill<16>(dst + C::kTileBytes, vp + off, live ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
+  };
+  auto group_sync = [&]() {
+    if constexpr (MT == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "r"(32 * MT) : "memory");
+  };
+  for (int i = 0; i < ST - 1; ++i) issue(i);
+
+  // ---------------------------------------------------------------- Q
+  // A fragments of the warp's 16 rows: lane (fg, ft) holds rows fg, fg + 8 at
+  // columns 2 ft, 2 ft + 1 and 8 + 2 ft, 9 + 2 ft of every 16
+  const int r0 = rt * 16 + fg, r1 = r0 + 8;
+  const T* qp = static_cast<const T*>(p.q) + int64_t(b) * p.q_sb;
+  auto q_row = [&](int r) -> const T* {
+    return qp + int64_t(kvh * p.group + r / p.q_tokens) * p.q_sn + int64_t(r % p.q_tokens) * p.q_ss;
+  };
+  uint32_t qa[KK][4];
+#pragma unroll
+  for (int kk = 0; kk < KK; ++kk) {
+    const int c = kk * 16 + 2 * ft;
+    qa[kk][0] = r0 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r0) + c) : 0u;
+    qa[kk][1] = r1 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r1) + c) : 0u;
+    qa[kk][2] = r0 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r0) + c + 8) : 0u;
+    qa[kk][3] = r1 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r1) + c + 8) : 0u;
+  }
+  const int p0 = first + r0 % p.q_tokens, p1 = first + r1 % p.q_tokens;   // the rows' positions
+  auto sees = [&](int pos, int j) -> bool {
+    return j <= pos && j >= p.base && (j < p.sink || int64_t(pos) - j <= p.pre);
+  };
+
+  // ---------------------------------------------------------------- the loop
+  float o[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  const float sl2 = p.scale_log2;
+  const int lr = lane & 7, lm = lane >> 3;
+  for (int i = 0; i < n; ++i) {
+    cp_async_wait_group<ST - 2>();
+    group_sync();            // the tile is in for every warp of the group, and the slot before it has been read
+    issue(i + ST - 1);
+    const uint32_t ks = ring + (i % ST) * C::kStageBytes, vs = ks + C::kTileBytes;
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      // matrices: keys 0-7 | 0-7 | 8-15 | 8-15, pieces 2 kk | 2 kk + 1 | ...
+      uint32_t f[4];
+      const int row = (lm >> 1) * 8 + lr, c = 2 * kk + (lm & 1);
+      ldsm4(ks + row * (D * 2) + ((c ^ lr) << 4), f);
+      mma16<BF16>(s[0], qa[kk], f[0], f[1]);
+      mma16<BF16>(s[1], qa[kk], f[2], f[3]);
+    }
+    const int j0 = tile_key(i);
+    // every row sees every key of the tile
+    const bool full = j0 + kSpanTile - 1 <= first && j0 >= p.base &&
+                      (j0 + kSpanTile <= p.sink || j0 >= win + p.q_tokens - 1);
+    if (!full) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = j0 + 8 * h + 2 * ft + e;
+          if (!sees(p0, j)) s[h][e] = -INFINITY;
+          if (!sees(p1, j)) s[h][2 + e] = -INFINITY;
+        }
+    }
+    float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+    float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+    const float n0 = fmaxf(m0, x0 * sl2), n1 = fmaxf(m1, x1 * sl2);
+    if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {
+      const float a0 = m0 == n0 ? 1.f : fast_exp2(m0 - n0), a1 = m1 == n1 ? 1.f : fast_exp2(m1 - n1);
+      l0 *= a0;
+      l1 *= a1;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[t][0] *= a0;
+        o[t][1] *= a0;
+        o[t][2] *= a1;
+        o[t][3] *= a1;
+      }
+      m0 = n0;
+      m1 = n1;
+    }
+    const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+    uint32_t pa[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float y0 = fast_exp2(fmaf(s[h][0], sl2, -z0)), y1 = fast_exp2(fmaf(s[h][1], sl2, -z0));
+      const float y2 = fast_exp2(fmaf(s[h][2], sl2, -z1)), y3 = fast_exp2(fmaf(s[h][3], sl2, -z1));
+      l0 += y0 + y1;
+      l1 += y2 + y3;
+      pa[2 * h] = pack2(y0, y1, BF16);
+      pa[2 * h + 1] = pack2(y2, y3, BF16);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; t += 2) {
+      // matrices: keys 0-7 | 8-15 of piece t, then of piece t + 1
+      uint32_t f[4];
+      const int row = (lm & 1) * 8 + lr, c = t + (lm >> 1);
+      ldsm4_trans(vs + row * (D * 2) + ((c ^ lr) << 4), f);
+      mma16<BF16>(o[t], pa, f[0], f[1]);
+      mma16<BF16>(o[t + 1], pa, f[2], f[3]);
+    }
+  }
+  cp_async_wait_all();
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+
+  // ---------------------------------------------------------------- join
+  // [group][16 MT rows][D] with the float4s of a row XOR-swizzled by row, so
+  // that the rows of a store instruction do not share banks
+  __syncthreads();           // every ring has been read
+  float* ob = reinterpret_cast<float*>(smem);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kOffML);
+  auto at = [&](int g, int r, int c4) -> int { return ((g * 16 * MT + r) * (D / 4) + (c4 ^ ((r & 7) << 1))) * 4; };
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int c = t * 8 + 2 * ft;
+    *reinterpret_cast<float2*>(ob + at(kg, r0, c >> 2) + (c & 3)) = make_float2(o[t][0], o[t][1]);
+    *reinterpret_cast<float2*>(ob + at(kg, r1, c >> 2) + (c & 3)) = make_float2(o[t][2], o[t][3]);
+  }
+  if (ft == 0) {
+    ml[kg * 16 * MT + r0] = make_float2(m0, l0);
+    ml[kg * 16 * MT + r1] = make_float2(m1, l1);
+  }
+  __syncthreads();
+  const int items = p.rows * (D / 4);
+  if (cs > 1) {
+    if (C::kGroups > 1) {
+      // this CTA's groups into group 0
+      float4 acc[(16 * MT * (D / 4) + kSpanThreads - 1) / kSpanThreads];
+      float2 mine = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int w = 0; w < (16 * MT * (D / 4)) / kSpanThreads; ++w) {
+        const int e = w * kSpanThreads + threadIdx.x;
+        if (e >= items) break;
+        const int r = e / (D / 4), c4 = e % (D / 4);
+        float top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) top = fmaxf(top, ml[g * 16 * MT + r].x);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+          const float wt = join_weight(ml[g * 16 * MT + r].x, top);
+          const float4 x = *reinterpret_cast<const float4*>(ob + at(g, r, c4));
+          a.x += wt * x.x; a.y += wt * x.y; a.z += wt * x.z; a.w += wt * x.w;
+        }
+        acc[w] = a;
+      }
+      if (int(threadIdx.x) < p.rows) {
+        const int r = threadIdx.x;
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) mine.x = fmaxf(mine.x, ml[g * 16 * MT + r].x);
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+          const float2 x = ml[g * 16 * MT + r];
+          mine.y += join_weight(x.x, mine.x) * x.y;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < (16 * MT * (D / 4)) / kSpanThreads; ++w) {
+        const int e = w * kSpanThreads + threadIdx.x;
+        if (e >= items) break;
+        *reinterpret_cast<float4*>(ob + at(0, e / (D / 4), e % (D / 4))) = acc[w];
+      }
+      if (int(threadIdx.x) < p.rows) ml[threadIdx.x] = mine;
+    }
+    cluster_sync_all();
+  }
+  const int n_own = cs > 1 ? int(cs) : C::kGroups;
+  const uint32_t ob_a = smem_u32(ob), ml_a = smem_u32(ml);
+  for (int e = int(rank) * kSpanThreads + threadIdx.x; e < items; e += int(cs) * kSpanThreads) {
+    const int r = e / (D / 4), c4 = e % (D / 4);
+    const int head = kvh * p.group + r / p.q_tokens, tokn = r % p.q_tokens;
+    const int64_t prow = (int64_t(b) * p.N1 + head) * p.q_tokens + tokn;
+    auto own_ml = [&](int g) -> float2 {
+      return cs > 1 ? ld_peer2(peer_addr(ml_a + r * 8, g)) : ml[g * 16 * MT + r];
+    };
+    float top = -INFINITY;
+    for (int g = 0; g < n_own; ++g) top = fmaxf(top, own_ml(g).x);
+    for (int g = 0; g < p.n_parts; ++g) top = fmaxf(top, p.part_ml[g * p.part_rows + prow].x);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int g = 0; g < n_own; ++g) {
+      const float2 x = own_ml(g);
+      const float w = join_weight(x.x, top);
+      const float4 y = cs > 1 ? ld_peer4(peer_addr(ob_a + at(0, r, c4) * 4, g))
+                              : *reinterpret_cast<const float4*>(ob + at(g, r, c4));
+      l += w * x.y;
+      a.x += w * y.x; a.y += w * y.y; a.z += w * y.z; a.w += w * y.w;
+    }
+    for (int g = 0; g < p.n_parts; ++g) {
+      const float2 x = p.part_ml[g * p.part_rows + prow];
+      const float w = join_weight(x.x, top);
+      const float4 y = *reinterpret_cast<const float4*>(p.part_o + (g * p.part_rows + prow) * D + c4 * 4);
+      l += w * x.y;
+      a.x += w * y.x; a.y += w * y.y; a.z += w * y.z; a.w += w * y.w;
+    }
+    const bool has = l != 0.f;   // a NaN sum stays a NaN
+    const float inv = has ? 1.f / l : 0.f;
+    uint2 u;
+    u.x = has ? pack2(a.x * inv, a.y * inv, BF16) : 0u;
+    u.y = has ? pack2(a.z * inv, a.w * inv, BF16) : 0u;
+    T* orow = static_cast<T*>(p.out) + int64_t(b) * p.q_sb + int64_t(head) * p.q_sn + int64_t(tokn) * p.q_ss;
+    *reinterpret_cast<uint2*>(orow + c4 * 4) = u;
+    if (p.lse != nullptr && c4 == 0)
+      p.lse[int64_t(b) * p.lse_sb + int64_t(head) * p.lse_sn + int64_t(tokn) * p.lse_ss] =
+          has ? (top + __log2f(l)) * 0.69314718055994531f : INFINITY;
+  }
+  if (cs > 1) cluster_sync_all();   // no CTA leaves while another reads its shared memory
+}
+
+template <int D, bool BF16, int MT>
+cudaError_t launch_one(const SpanParams& p, int cs, cudaStream_t s) {
+  using C = SpanCfg<D, MT>;
+  cudaError_t e = set_smem_once<span_decode_kernel<D, BF16, MT>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.B * p.N2 * cs));
+  cfg.blockDim = dim3(kSpanThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(cs);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, span_decode_kernel<D, BF16, MT>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_span_decode(const SpanParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s) {
+  const int mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+  // CTAs of a unit: enough to fill the GPU (two CTAs per SM), as long as a
+  // group keeps two tiles
+  const int64_t span = std::min<int64_t>(p.kv_max - p.base, int64_t(p.sink) + p.pre + p.q_tokens);
+  const int64_t tiles = span / kSpanTile + 1;
+  const int64_t units = int64_t(p.B) * p.N2;
+  int cs = 1;
+  while (cs < 8 && units * cs < 2 * n_sm && tiles >= int64_t(4) * cs * (4 / mt)) cs *= 2;
+#define FIA_SPAN(DD, BB)                                    \
+  switch (mt) {                                             \
+    case 1: return launch_one<DD, BB, 1>(p, cs, s);         \
+    case 2: return launch_one<DD, BB, 2>(p, cs, s);         \
+    default: return launch_one<DD, BB, 4>(p, cs, s);        \
+  }
+  if (head_dim == 128) {
+    if (bf16) { FIA_SPAN(128, true) } else { FIA_SPAN(128, false) }
+  }
+  if (bf16) { FIA_SPAN(64, true) } else { FIA_SPAN(64, false) }
+#undef FIA_SPAN
+}
+
+}  // namespace fia

@@ -323,6 +323,81 @@ FIA_API fia_status bsa_forward_fp8(const fia_tensor* query, const fia_tensor* ke
                            const fia_tensor* attention_out, const fia_tensor* softmax_lse, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged serving.  The operators from here to fia_decode_shared_prefix take
+ * every length from DEVICE memory (int32), so their launches depend on sizes
+ * alone: a captured step replays with new lengths.  A step runs them in this
+ * order: tables and slots from the requests' lengths, the write of the new
+ * keys and values, attention over the cache.
+ *
+ * fia_block_table_append: grows the block tables of B requests and gives every
+ * new token its slot.
+ *   context_lens, new_lens: int32 (B); tokens the cache holds of a request, and
+ *          tokens to append (negative: 0).  Request b holds ceil(context /
+ *          block_size) blocks and needs ceil((context + new) / block_size).
+ *   free_blocks: int32 (F), ids handed out from the front, in request order.
+ *   block_table: int32 (B, W), in place: the columns of the blocks that a
+ *          request lacked are written, every other entry stays as it was.
+ *   slot_mapping: int32 (T), out: slot block_id * block_size + offset of every
+ *          new token, the requests' tokens one after the other; -1 from the
+ *          sum of new_lens on (a padded batch).  Tokens past T get no slot,
+ *          and a block whose first token is past T no entry.
+ *   kv_lens: int32 (B), out: context + new.   cu_new_lens: int32 (B), out:
+ *          running sum of new_lens without a leading 0 (the TND lists' form).
+ *   num_blocks: int32 (1), out: blocks the batch asked for.  Above F the list
+ *          ran out: the entries of blocks without an id are written as -1
+ *          and their tokens' slots are -1, as they are for a token past the
+ *          table's last column.
+ *   block_size: 1 or more.  Outputs may not overlap the inputs.
+ * ------------------------------------------------------------------------ */
+FIA_API fia_status fia_block_table_append(const fia_tensor* context_lens, const fia_tensor* new_lens,
+                                  const fia_tensor* free_blocks, int64_t block_size, const fia_tensor* block_table,
+                                  const fia_tensor* slot_mapping, const fia_tensor* kv_lens,
+                                  const fia_tensor* cu_new_lens, const fia_tensor* num_blocks, void* stream);
+
+/* ------------------------------------------------------------------------
+ * fia_cache_write: copies new keys and values to their slots of the pools.
+ *   key (T, KV_N, D), value (T, KV_N, Dv): f16, bf16 or e4m3; heads and
+ *          columns contiguous, tokens key_token_stride / value_token_stride
+ *          elements apart (0: contiguous; slices of a fused projection have
+ *          its row length), rows 16-byte aligned.  D * element size is a
+ *          multiple of 16.  value and value_cache may both be NULL.
+ *   key_cache / value_cache: (blocknum, KV_N, block_size, D) or (blocknum,
+ *          block_size, KV_N*D), the same blocknum and block_size, the
+ *          tensors' types.
+ *   slot_mapping: int32 (T): token t goes to row slot % block_size of block
+ *          slot / block_size.  Slots outside the pool (negative ones among
+ *          them) are skipped; every other row of the pools stays as it was.
+ *          Slots must differ: of two tokens with one slot either may be left,
+ *          or a mixture.
+ * ------------------------------------------------------------------------ */
+FIA_API fia_status fia_cache_write(const fia_tensor* key, int64_t key_token_stride, const fia_tensor* value,
+                           int64_t value_token_stride, const fia_tensor* key_cache, const fia_tensor* value_cache,
+                           const fia_tensor* slot_mapping, void* stream);
+
+/* ------------------------------------------------------------------------
+ * fia_decode_window: incremental attention with a sliding window and sink
+ * tokens.  Token i of a sequence's Q_S new tokens has position p = L - Q_S + i
+ * and sees key j when j <= p and (j >= p - pre_tokens or j < sink_tokens).
+ *   query, attention_out, softmax_lse: as fia_decode (BNSD / BSND / BSH, Q_S
+ *          1..16, Q_N / KV_N * Q_S <= 64, D 64 or 128).
+ *   key/value, contiguous or paged: as fia_decode (block_size a multiple of
+ *          16).  Block ids outside the pool read as zeros; entries of blocks
+ *          that no token sees are never read, so blocks behind the window may
+ *          be freed.  At most 2^30 keys per sequence.
+ *   actual_seq_kvlen: device int32 (B), the length L with the new tokens,
+ *          clamped to [0, keys the tensors have room for]; NULL: all of them
+ *          (contiguous key/value only).  params' own lists must be NULL.
+ *   params->pre_tokens >= 0 (default 2^31-1: no window), sink_tokens >= 0.
+ *          sparse_mode and next_tokens are not read.
+ *   Rows that see no key (p < 0: a padded batch) give 0 and +inf.
+ *   No workspace.
+ * ------------------------------------------------------------------------ */
+FIA_API fia_status fia_decode_window(const fia_tensor* query, const fia_tensor* key, const fia_tensor* value,
+                             const fia_tensor* block_table, const fia_tensor* actual_seq_kvlen,
+                             const fia_params* params, int64_t sink_tokens, const fia_tensor* attention_out,
+                             const fia_tensor* softmax_lse, void* stream);
+
 /* Waits for `stream`, then returns the device-side status recorded in a
  * workspace by the last call that used it (FIA_OK or FIA_ERR_TIMEOUT). */
 FIA_API fia_status fia_device_status(const void* workspace, void* stream);

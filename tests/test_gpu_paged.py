@@ -1,0 +1,264 @@
+"""Block tables and slot maps, the cache write and windowed decode on the GPU
+against the plain oracle: whole values equal, attention within the bounds that
+its roundings give."""
+import numpy as np
+import pytest
+import torch
+
+import fia_inputs
+from oracle import paged_oracle as po
+from oracle.fia_oracle import f64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ block tables and slots
+def _tables(fia, ctx, new, bs, W=None, free=None, n_tokens=None, fill=-7):
+    rng = np.random.default_rng(len(ctx) + bs)
+    tot = [max(a, 0) + max(b, 0) for a, b in zip(ctx, new)]
+    W = max([-(-t // bs) for t in tot] + [1]) if W is None else W
+    need = sum(-(-t // bs) for t in tot)
+    ids = rng.permutation(need + 5)
+    table = np.full((len(ctx), W), fill, dtype=np.int64)
+    at = 0
+    for b, c in enumerate(ctx):
+        n = min(-(-max(c, 0) // bs), W)
+        table[b, :n] = ids[at:at + n]
+        at += n
+    free = list(ids[at:]) if free is None else free
+    T = sum(max(a, 0) for a in new) if n_tokens is None else n_tokens
+    ref = po.block_table_append(ctx, new, free, table, bs, T)
+    dt = torch.from_numpy(table).int().to(DEV)
+    got = fia.fia_block_table_append(i32(ctx), i32(new), i32(free), dt, block_size=bs, num_tokens=T)
+    torch.cuda.synchronize()
+    assert np.array_equal(dt.cpu().numpy(), ref[0])
+    for g, r in zip(got, ref[1:]):
+        assert g.cpu().tolist() == (list(r) if not isinstance(r, int) else [r])
+    return got, dt
+
+
+@pytest.mark.parametrize("bs", [1, 16, 100, 128])
+def test_tables_ragged(fia, bs):
+    _tables(fia, [0, 1, bs - 1, bs, bs + 1, 3 * bs, 1000], [1, 0, 1, 1, 2 * bs, bs + 3, 777], bs)
+
+
+@pytest.mark.parametrize("B", [1, 3, 1023, 1024, 1025, 2500])
+def test_tables_batch_sizes(fia, B):
+    """Across the 1024-request chunk of the scan, tokens across CTAs."""
+    r = np.random.default_rng(B)
+    _tables(fia, r.integers(0, 90, B).tolist(), r.integers(0, 5, B).tolist(), 16)
+
+
+def test_tables_one_long_request(fia):
+    _tables(fia, [5, 17, 0], [0, 5000, 2], 16)
+
+
+def test_tables_padding_and_undersized(fia):
+    """More slots than tokens are -1; fewer: the rest of the tokens get nothing."""
+    _tables(fia, [3, 9], [5, 7], 4, n_tokens=40)
+    _tables(fia, [3, 9], [5, 7], 4, n_tokens=6)
+    _tables(fia, [3, 9], [5, 7], 4, n_tokens=0)
+
+
+def test_tables_short_list_and_narrow_table(fia):
+    (_, _, _, blocks), _ = _tables(fia, [0, 4, 8], [9, 9, 9], 4, free=[11, 5, 3])
+    assert blocks.item() > 3
+    _tables(fia, [0, 4, 8], [9, 9, 9], 4, W=3)
+    _tables(fia, [0, 4, 8], [9, 9, 9], 4, free=[])
+
+
+def test_tables_negative_and_empty(fia):
+    _tables(fia, [-3, 4], [2, -9], 4)
+    got, _ = _tables(fia, [], [], 16, n_tokens=3)
+    assert got[3].item() == 0
+
+
+def test_tables_lengths_near_int32(fia):
+    """A running position past 2^31 is clamped, not wrapped."""
+    big = 2 ** 31 - 2
+    s, kv, cu, nb = fia.fia_block_table_append(i32([big, 5]), i32([4, 2]), i32([7, 8]), i32([[0, 0], [1, 1]]),
+                                               block_size=1 << 20, num_tokens=6)
+    assert kv.tolist() == [2 ** 31 - 1, 7] and cu.tolist() == [4, 6]
+    assert s.tolist() == [-1, -1, -1, -1, (1 << 20) + 5, (1 << 20) + 6]
+
+
+# ------------------------------------------------------------------ cache write
+@pytest.mark.parametrize("pool", ["BNBD", "BBH"])
+@pytest.mark.parametrize("n2,d,dt,bs,T", [(8, 128, "bf16", 128, 300), (1, 64, "f16", 16, 1), (3, 72, "bf16", 5, 77),
+                                          (2, 512, "f16", 64, 65), (5, 128, "bf16", 16, 1030)])
+def test_write(fia, pool, n2, d, dt, bs, T):
+    nb = 2 * (-(-T // bs)) + 1
+    shape = (nb, n2, bs, d) if pool == "BNBD" else (nb, bs, n2 * d)
+    kc, vc = (fia_inputs.normal(shape, dt, 70, i) for i in (1, 2))
+    x = fia_inputs.normal((T, 4 * n2, d), dt, 71, 3)
+    slots = np.random.default_rng(T).permutation(nb * bs)[:T]
+    slots[T // 2::7] = -1
+    slots[3::50] = nb * bs + 5      # past the pool: skipped
+    xd = x.to(DEV)
+    k, v = xd[:, n2:2 * n2], xd[:, 3 * n2:]   # slices of one projection
+    a, b = kc.to(DEV), vc.to(DEV)
+    got = fia.fia_cache_write(k, v, a, b, i32(slots.tolist()))
+    assert got[0] is a and got[1] is b
+    for y, c, z in ((x[:, n2:2 * n2], kc, a), (x[:, 3 * n2:], vc, b)):
+        ref = po.cache_write(f64(y), f64(c), slots.tolist())
+        assert np.array_equal(f64(z.cpu()), ref)
+
+
+def test_write_latent_and_rope(fia):
+    """Keys and values of different head dims (a latent cache and its rope part), and keys alone."""
+    T, bs, nb = 50, 16, 8
+    lat, rope = (fia_inputs.normal((T, 1, d), "bf16", 72, d).to(DEV) for d in (512, 64))
+    cl, cr = torch.zeros(nb, bs, 512, dtype=torch.bfloat16, device=DEV), torch.zeros(nb, bs, 64, dtype=torch.bfloat16, device=DEV)
+    slots = np.random.default_rng(1).permutation(nb * bs)[:T]
+    fia.fia_cache_write(lat, rope, cl, cr, i32(slots.tolist()))
+    assert torch.equal(cl.view(-1, 512)[slots], lat[:, 0]) and torch.equal(cr.view(-1, 64)[slots], rope[:, 0])
+    only = torch.zeros_like(cl)
+    fia.fia_cache_write(lat, None, only, None, i32(slots.tolist()))
+    assert torch.equal(only, cl)
+
+
+def test_write_e4m3(fia):
+    T, bs = 9, 16
+    x = torch.randn(T, 2, 64, device=DEV).to(torch.float8_e4m3fn)
+    c = torch.zeros(3, 2, bs, 64, device=DEV).to(torch.float8_e4m3fn)
+    fia.fia_cache_write(x, None, c, None, i32(list(range(20, 20 + T))))
+    assert torch.equal(c.view(torch.uint8).transpose(1, 2).reshape(-1, 2, 64)[20:20 + T], x.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ windowed decode
+def _window(fia, lens, n1, n2, D, pre, sink, Q=1, bs=128, dt="bf16", kv="BNBD", layout="BNSD", workload=80, evict=True):
+    """A paged case whose unseen blocks are taken out of the tables (id -1 or far outside) and whose unseen rows are
+    NaN: only what the tokens see may be read into the result."""
+    c = fia_inputs.paged_decode_case(len(lens), n1, n2, D, lens, block_size=bs, dtype=dt, workload=workload, layout_kv=kv,
+                                     q_tokens=Q)
+    rows, table = [], c.block_table.clone()
+    kp, vp = c.k_pool.clone(), c.v_pool.clone()
+    for b, L in enumerate(lens):
+        rows.append(tuple(po.cache_rows(f64(x), c.block_table[b], L, n2) for x in (c.k_pool, c.v_pool)))
+        seen = po.window_see(Q, L, pre, sink).any(0) if L else np.zeros(0, bool)
+        for i in range(-(-L // bs)):
+            s = seen[i * bs:(i + 1) * bs]
+            blk = int(c.block_table[b, i])
+            for x in (kp, vp):
+                y = x[blk] if x.dim() == 3 else x[blk].transpose(0, 1)
+                y[:len(s)][torch.from_numpy(~s)] = float("nan")
+            if evict and not s.any():
+                table[b, i] = -1 if i % 2 else 2 ** 31 - 1
+    q = c.q if layout == "BNSD" else c.q.transpose(1, 2).contiguous()
+    q = q.flatten(2) if layout == "BSH" else q
+    out, lse = fia.fia_decode_window(q.to(DEV), kp.to(DEV), vp.to(DEV), block_table=table.to(DEV), block_size=bs,
+                                     actual_seq_kvlen=i32(lens), num_heads=n1, num_key_value_heads=n2, scale_value=c.scale,
+                                     input_layout=layout, pre_tokens=pre, sink_tokens=sink, softmax_lse_flag=True)
+    torch.cuda.synchronize()
+    out = out.reshape(len(lens), Q, n1, D).transpose(1, 2) if layout != "BNSD" else out
+    ref = po.decode(c.q, rows, lens, pre, sink, c.scale)
+    po.assert_close(out, lse, ref)
+    return out, lse
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("pre,sink", [(0, 0), (0, 1), (15, 4), (16, 16), (100, 0), (127, 130), (1000, 3), (BIG, 0),
+                                      (BIG, BIG), (40, BIG)])
+def test_window_masks(fia, pre, sink):
+    _window(fia, [1, 2, 16, 17, 300, 0, 513, 1999], 8, 2, 128, pre, sink)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 48, 64, 256])
+@pytest.mark.parametrize("kv", ["BNBD", "BBH"])
+def test_window_pages(fia, bs, kv):
+    _window(fia, [1, 40, 333, 777], 8, 4, 128, 99, 5, bs=bs, kv="BNBD" if kv == "BNBD" else "BSH")
+
+
+@pytest.mark.parametrize("n1,n2,Q", [(4, 4, 1), (6, 2, 3), (14, 2, 2), (16, 1, 1), (17, 1, 1), (32, 1, 1), (8, 2, 8), (33, 1, 1),
+                                     (64, 1, 1), (8, 2, 16), (16, 1, 4), (5, 5, 16)])
+def test_window_rows(fia, n1, n2, Q):
+    """Units of 1..64 rows: one, two and four row tiles."""
+    _window(fia, [max(Q, 1), 130, 555], n1, n2, 128, 70, 9, Q=Q, workload=81 + n1)
+
+
+@pytest.mark.parametrize("dt,D", [("f16", 128), ("bf16", 64), ("f16", 64)])
+@pytest.mark.parametrize("n1,Q", [(4, 1), (20, 1), (16, 4)])
+def test_window_types(fia, dt, D, n1, Q):
+    _window(fia, [64, 700, 18], n1, 1, D, 200, 4, Q=Q, dt=dt)
+
+
+@pytest.mark.parametrize("layout", ["BSND", "BSH"])
+def test_window_layouts(fia, layout):
+    _window(fia, [12, 300], 8, 2, 128, 50, 2, Q=3, layout=layout)
+
+
+def test_window_shorter_than_tokens(fia):
+    """A length below Q_S: the tokens before the sequence's start see nothing."""
+    out, lse = _window(fia, [0, 1, 3, 4, 90], 4, 2, 128, 30, 2, Q=4)
+    assert torch.isposinf(lse[0]).all() and (out[0] == 0).all()
+
+
+@pytest.mark.parametrize("B,n2", [(1, 1), (1, 8), (40, 8), (130, 4)])
+def test_window_cluster_sizes(fia, B, n2):
+    """Few to many units: clusters of 8 CTAs down to single CTAs; long spans, lengths from 0 up."""
+    lens = [(i * 977) % 2600 for i in range(B)]
+    lens[0] = 2600
+    _window(fia, lens, 2 * n2, n2, 64, 2000, 20, bs=64, workload=95)
+
+
+@pytest.mark.parametrize("layout", ["BNSD", "BSND", "BSH"])
+def test_window_contiguous(fia, layout):
+    B, n1, n2, S, D, Q = 3, 8, 2, 333, 128, 2
+    q = fia_inputs.normal((B, n1, Q, D), "bf16", 82, 1)
+    k, v = (fia_inputs.normal((B, n2, S, D), "bf16", 82, i) for i in (2, 3))
+    scale = D ** -0.5
+    lay = {"BNSD": lambda x: x, "BSND": lambda x: x.transpose(1, 2).contiguous(),
+           "BSH": lambda x: x.transpose(1, 2).flatten(2).contiguous()}[layout]
+    for lens in ([333, 2, 100], None):
+        out, lse = fia.fia_decode_window(lay(q).to(DEV), lay(k).to(DEV), lay(v).to(DEV),
+                                         actual_seq_kvlen=None if lens is None else i32(lens), num_heads=n1,
+                                         num_key_value_heads=n2, scale_value=scale, input_layout=layout, pre_tokens=60,
+                                         sink_tokens=7, softmax_lse_flag=True)
+        if layout != "BNSD":
+            out = out.reshape(B, Q, n1, D).transpose(1, 2)
+        rows = [tuple(f64(x[b].transpose(0, 1)) for x in (k, v)) for b in range(B)]
+        po.assert_close(out, lse, po.decode(q, rows, lens or [S] * B, 60, 7, scale))
+
+
+def test_window_lengths_beyond_the_tables_are_clamped(fia):
+    c = fia_inputs.paged_decode_case(1, 2, 1, 64, [96], block_size=32, workload=83, extra_table_cols=0)
+    kw = dict(block_table=c.block_table.to(DEV), block_size=32, num_heads=2, num_key_value_heads=1, scale_value=c.scale,
+              input_layout="BNSD")
+    args = [x.to(DEV) for x in (c.q, c.k_pool, c.v_pool)]
+    a, _ = fia.fia_decode_window(*args, actual_seq_kvlen=i32([96]), **kw)
+    b, _ = fia.fia_decode_window(*args, actual_seq_kvlen=i32([2 ** 31 - 1]), **kw)
+    z, _ = fia.fia_decode_window(*args, actual_seq_kvlen=i32([-5]), **kw)
+    assert torch.equal(a, b) and (z == 0).all()
+
+
+def test_window_without_window_equals_decode(fia):
+    """No window: fia_decode on the same cache, to the rounding of both."""
+    c = fia_inputs.paged_decode_case(5, 32, 8, 128, [1, 700, 2048, 33, 1500], workload=84)
+    args = [x.to(DEV) for x in (c.q, c.k_pool, c.v_pool)]
+    kw = dict(block_table=c.block_table.to(DEV), block_size=128, num_heads=32, num_key_value_heads=8, scale_value=c.scale,
+              input_layout="BNSD", softmax_lse_flag=True)
+    a, la = fia.fia_decode(*args, actual_seq_kvlen=c.kv_lens, **kw)
+    b, lb = fia.fia_decode_window(*args, actual_seq_kvlen=i32(c.kv_lens), **kw)
+    # each is off by at most half a step of the output and of the weights: |v| < 6 bounds sum w |v|
+    assert (a.float() - b.float()).abs().max() <= 4 * 2 ** -8 * 6 and (la - lb).abs().max() < 1e-4
+    again, _ = fia.fia_decode_window(*args, actual_seq_kvlen=i32(c.kv_lens), **kw)
+    assert torch.equal(b, again)
+
+
+def test_window_infinite_values_stay_where_they_are_seen(fia):
+    """An infinity or NaN in a seen value row reaches the rows that see it and no others."""
+    B, n1, D, S = 2, 2, 64, 200
+    q, k, v = (fia_inputs.normal((B, n, s, D), "bf16", 85, i) for i, (n, s) in enumerate(((n1, 1), (n1, S), (n1, S))))
+    v[0, 0, 150, 3] = float("inf")
+    v[0, 1, 20, 5] = float("nan")     # behind the window
+    out, _ = fia.fia_decode_window(*[x.to(DEV) for x in (q, k, v)], num_heads=n1, scale_value=0.125, input_layout="BNSD",
+                                   pre_tokens=99, sink_tokens=2)
+    assert torch.isposinf(out[0, 0, 0, 3]) and torch.isfinite(out[1]).all() and torch.isfinite(out[0, 1]).all()
+    assert torch.isfinite(out[0, 0, 0, :3]).all()
