@@ -18,6 +18,7 @@ from ._binding import INT32_MAX, _dtype_code, _lse_shape, _params, _stream_ptr, 
 # fia_tensor: data, dtype, ndim, shape[5].  A packed byte string is passed where
 # the call takes a const fia_tensor* (a tenth of the cost of a ctypes struct).
 _PACK = struct.Struct("<Qii5q").pack
+STATUS_BYTES = 256   # workspace of a call that needs no more than its status word
 _PAD = ((0,) * 5, (0,) * 4, (0,) * 3, (0,) * 2, (0,), ())
 
 
@@ -136,4 +137,32 @@ def fia_decode_window(query, key, value, *, actual_seq_kvlen=None, block_table=N
             _desc(query, "query"), _desc(key, "key"), _desc(value, "value"), _desc(block_table, "block_table"),
             _desc(actual_seq_kvlen, "actual_seq_kvlen"), ctypes.byref(prm.p), sink_tokens, _desc(out, "out"),
             _desc(softmax_lse, "softmax_lse"), stream))
+    return out, softmax_lse
+
+
+def fia_prefill_window(query, key, value, *, actual_seq_qlen=None, actual_seq_kvlen=None, block_table=None, block_size=0,
+                       num_heads=1, num_key_value_heads=0, scale_value=1.0, input_layout="BSH", pre_tokens=INT32_MAX,
+                       sink_tokens=0, softmax_lse_flag=False, out=None, softmax_lse=None, workspace=None):
+    """Prefill (any Q_S) with a sliding window and sink tokens: row i of a batch,
+    at position p = i + kv_len - q_len, sees key j when j <= p and (j >= p -
+    pre_tokens or j < sink_tokens).  actual_seq_qlen / actual_seq_kvlen: int32
+    CUDA tensors (B); for a TND query, and TND keys, running sums.  key / value
+    contiguous, or pools with block_table as for fia_prefill_paged.  Returns
+    (attention_out, softmax_lse or None)."""
+    import torch
+    with _on(query, key, value, actual_seq_qlen, actual_seq_kvlen, block_table, out, softmax_lse, workspace) as stream:
+        prm = _params(num_heads=num_heads, num_key_value_heads=num_key_value_heads, scale_value=scale_value,
+                      input_layout=input_layout, pre_tokens=pre_tokens, block_size=block_size,
+                      softmax_lse_flag=softmax_lse_flag)
+        if out is None:
+            out = torch.empty_like(query)
+        if softmax_lse_flag and softmax_lse is None:
+            softmax_lse = query.new_empty(_lse_shape(query, input_layout, num_heads), dtype=torch.float32)
+        if workspace is None:   # the status word
+            workspace = query.new_empty(STATUS_BYTES, dtype=torch.uint8)
+        check(load_library().fia_prefill_window(
+            _desc(query, "query"), _desc(key, "key"), _desc(value, "value"), _desc(block_table, "block_table"),
+            _desc(actual_seq_qlen, "actual_seq_qlen"), _desc(actual_seq_kvlen, "actual_seq_kvlen"), ctypes.byref(prm.p),
+            sink_tokens, _desc(out, "out"), _desc(softmax_lse, "softmax_lse"), workspace.data_ptr(), workspace.numel(),
+            stream))
     return out, softmax_lse

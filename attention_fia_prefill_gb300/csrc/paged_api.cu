@@ -166,6 +166,105 @@ fia_status span_params(const fia_tensor* q, const fia_tensor* k, const fia_tenso
   return FIA_OK;
 }
 
+// Arguments of fia_prefill_window -> launch parameters without the tensor maps.
+struct WindowPrefill {
+  PrefillParams p;
+  Layout layout;
+  int64_t B, N1, N2, S1, S2, D, blocks, bs;
+  bool bnbd;
+};
+
+fia_status window_prefill(const fia_tensor* q, const fia_tensor* k, const fia_tensor* v, const fia_tensor* table,
+                          const fia_tensor* qlen, const fia_tensor* kvlen, const fia_params* prm, int64_t sink,
+                          const fia_tensor* out, const fia_tensor* lse, WindowPrefill& w) {
+  memset(&w, 0, sizeof(w));
+  if (prm == nullptr) return fail(FIA_ERR_NULL, "params is NULL");
+  if (!given(q) || !given(k) || !given(v) || !given(out))
+    return fail(FIA_ERR_NULL, "query/key/value/attention_out required");
+  const Layout L = w.layout = parse_layout(prm->input_layout);
+  if (L == L_BAD) return fail(FIA_ERR_LAYOUT, "input_layout '%s' not supported", prm->input_layout);
+  if (!is_half(q->dtype) || k->dtype != q->dtype || v->dtype != q->dtype || out->dtype != q->dtype)
+    return fail(FIA_ERR_DTYPE, "query/key/value/attention_out must share fp16 or bf16");
+  if (prm->actual_seq_qlen != nullptr || prm->actual_seq_kvlen != nullptr)
+    return fail(FIA_ERR_SEQLEN, "lengths are a device tensor here: params' actual_seq lists must be NULL");
+  FIA_TRY(resolve_heads(prm, w.N1, w.N2));
+  if (!same_shape(q, out)) return fail(FIA_ERR_SHAPE, "attention_out must have the query's shape");
+  if (!same_shape(k, v)) return fail(FIA_ERR_SHAPE, "key and value shapes differ");
+  FIA_TRY(dense_dims(q, L, w.N1, w.B, w.S1, w.D, "query"));
+  if (w.D != 64 && w.D != 128) return fail(FIA_ERR_UNSUPPORTED, "head dim %lld (kernels take 64 or 128)", (long long)w.D);
+  if (!(prm->scale_value > 0.0) || !std::isfinite(prm->scale_value))
+    return fail(FIA_ERR_UNSUPPORTED, "scale_value must be finite and > 0");
+  if (prm->pre_tokens < 0) return fail(FIA_ERR_UNSUPPORTED, "pre_tokens must be 0 or more");
+  if (sink < 0) return fail(FIA_ERR_UNSUPPORTED, "sink_tokens must be 0 or more");
+  if (!aligned16(q->data) || !aligned16(k->data) || !aligned16(v->data) || !aligned16(out->data))
+    return fail(FIA_ERR_ALIGNMENT, "query/key/value/attention_out must be 16-byte aligned");
+  const bool tnd = L == L_TND, lens_q = qlen != nullptr && qlen->ndim > 0, lens_k = kvlen != nullptr && kvlen->ndim > 0;
+  if (tnd) {
+    if (!lens_q) return fail(FIA_ERR_SEQLEN, "actual_seq_qlen is required for TND");
+    FIA_TRY(check_i32(qlen, -1, "actual_seq_qlen"));
+    w.B = qlen->shape[0];
+    if (w.B > 4096) return fail(FIA_ERR_SEQLEN, "actual_seq_qlen has %lld entries (> 4096)", (long long)w.B);
+  } else if (lens_q) {
+    FIA_TRY(check_i32(qlen, w.B, "actual_seq_qlen"));
+  }
+  const bool paged = table != nullptr && table->ndim > 0;
+  if (paged) {
+    if (table->dtype != FIA_DTYPE_I32 || table->ndim != 2 || table->shape[0] != w.B || !given(table) || table->shape[1] < 1)
+      return fail(FIA_ERR_BLOCK_TABLE, "block_table must be int32 (B, maxBlocksPerSeq)");
+    if (reinterpret_cast<uintptr_t>(table->data) % 4 != 0) return fail(FIA_ERR_ALIGNMENT, "block_table not 4-byte aligned");
+    if (!lens_k) return fail(FIA_ERR_SEQLEN, "page attention needs actual_seq_kvlen");
+    w.bs = prm->block_size;
+    if (w.bs < 128 || w.bs > 512 || w.bs % 128 != 0)
+      return fail(FIA_ERR_BLOCK_TABLE, "block_size %lld: 128..512, a multiple of 128", (long long)w.bs);
+    w.bnbd = k->ndim == 4;
+    if (w.bnbd ? (k->shape[1] != w.N2 || k->shape[2] != w.bs || k->shape[3] != w.D)
+               : (k->ndim != 3 || k->shape[1] != w.bs || k->shape[2] != w.N2 * w.D))
+      return fail(FIA_ERR_SHAPE, "paged key must be (blocknum, KV_N, block_size, D) or (blocknum, block_size, KV_N*D)");
+    w.blocks = k->shape[0];
+    w.S2 = table->shape[1] > kMaxKeys / w.bs ? kMaxKeys + 1 : table->shape[1] * w.bs;
+    FIA_TRY(check_i32(kvlen, w.B, "actual_seq_kvlen"));
+  } else {
+    int64_t Bk, Dk;
+    FIA_TRY(dense_dims(k, L, w.N2, Bk, w.S2, Dk, "key"));
+    if (Dk != w.D || (!tnd && Bk != w.B)) return fail(FIA_ERR_SHAPE, "key must be (B, ..., D) like the query");
+    if (tnd && !lens_k) return fail(FIA_ERR_SEQLEN, "actual_seq_kvlen is required for TND");
+    if (lens_k) FIA_TRY(check_i32(kvlen, w.B, "actual_seq_kvlen"));
+  }
+  if (w.S1 > kMaxKeys || w.S2 > kMaxKeys) return fail(FIA_ERR_SHAPE, "more than 2^30 rows or keys");
+  FIA_TRY(check_lse(lse, prm, L, w.B, w.N1, w.S1, w.S1));
+  PrefillParams& p = w.p;
+  int64_t os[3];
+  bns_strides(L, w.N1, w.S1, w.D, os);
+  p.out = out->data;
+  p.out_sb = os[0]; p.out_sn = os[1]; p.out_ss = os[2];
+  if (prm->softmax_lse_flag != 0) p.lse = static_cast<float*>(lse->data);
+  p.lse_sb = tnd ? 0 : w.N1 * w.S1;
+  p.lse_sn = tnd ? 1 : w.S1;
+  p.lse_ss = tnd ? w.N1 : 1;
+  // pairs of query tiles: TND has at most one part-filled pair a batch
+  const int64_t pairs = tnd ? w.S1 / (2 * kTileM) + std::min(w.B, w.S1) : w.B * ((w.S1 + 2 * kTileM - 1) / (2 * kTileM));
+  if (pairs * w.N1 > kMaxInt) return fail(FIA_ERR_SHAPE, "query is too large");
+  p.n_items = int(pairs * w.N1);
+  p.num_heads = int(w.N1);
+  p.num_kv_heads = int(w.N2);
+  p.group = int(w.N1 / w.N2);
+  p.is_tnd = tnd;
+  p.band_pre = int(std::min<int64_t>(prm->pre_tokens, kMaxKeys));
+  p.sink = int(std::min<int64_t>(sink, w.S2));
+  p.q_lens = lens_q ? static_cast<const int32_t*>(qlen->data) : nullptr;
+  p.kv_lens = lens_k ? static_cast<const int32_t*>(kvlen->data) : nullptr;
+  p.n_batch = int(w.B);
+  p.s1 = int(w.S1);
+  p.s2 = int(w.S2);
+  p.scale_log2 = float(prm->scale_value * 1.4426950408889634);
+  if (paged) {
+    p.block_table = static_cast<const int32_t*>(table->data);
+    p.table_stride = table->shape[1];
+    p.block_size = int(w.bs);
+  }
+  return FIA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -257,6 +356,64 @@ fia_status fia_decode_window(const fia_tensor* query, const fia_tensor* key, con
   return cuda_check(
       profiled(s, [&] { return launch_span_decode(p, int(D), query->dtype == FIA_DTYPE_BF16, sm_count(), s); }),
       "window decode launch");
+}
+
+fia_status fia_prefill_window_get_workspace_size(const fia_tensor* query, const fia_tensor* key,
+                                                 const fia_tensor* value, const fia_tensor* block_table,
+                                                 const fia_tensor* actual_seq_qlen,
+                                                 const fia_tensor* actual_seq_kvlen, const fia_params* params,
+                                                 int64_t sink_tokens, const fia_tensor* attention_out,
+                                                 const fia_tensor* softmax_lse, size_t* workspace_bytes) {
+  if (workspace_bytes == nullptr) return fail(FIA_ERR_NULL, "workspace_bytes is NULL");
+  *workspace_bytes = kHeader;
+  if (query != nullptr && query->ndim > 0 && numel(query) == 0) return FIA_OK;   // empty query
+  WindowPrefill w;
+  return window_prefill(query, key, value, block_table, actual_seq_qlen, actual_seq_kvlen, params, sink_tokens,
+                        attention_out, softmax_lse, w);
+}
+
+fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor* key, const fia_tensor* value,
+                              const fia_tensor* block_table, const fia_tensor* actual_seq_qlen,
+                              const fia_tensor* actual_seq_kvlen, const fia_params* params, int64_t sink_tokens,
+                              const fia_tensor* attention_out, const fia_tensor* softmax_lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (query != nullptr && query->ndim > 0 && numel(query) == 0) return FIA_OK;
+  WindowPrefill w;
+  FIA_TRY(window_prefill(query, key, value, block_table, actual_seq_qlen, actual_seq_kvlen, params, sink_tokens,
+                         attention_out, softmax_lse, w));
+  FIA_TRY(check_ws(workspace, workspace_bytes, kHeader));
+  if (w.p.n_items == 0) return FIA_OK;   // a TND query without sequences
+  PrefillParams& p = w.p;
+  const int64_t Bmap = w.layout == L_TND ? 1 : w.B;
+  FIA_TRY(dense_map(&p.tm_q, query, w.layout, Bmap, w.N1, w.S1, w.D));
+  // K/V without a row: no kernel reads them, but a map wants an extent
+  fia_tensor kk = *key, vv = *value;
+  int64_t rows = w.S2, blocks = w.blocks;
+  if (numel(key) == 0) {
+    kk.data = vv.data = query->data;
+    p.kv_lens = nullptr;
+    p.s2 = 0;
+    p.block_table = nullptr;
+    p.tm_k = p.tm_v = p.tm_q;
+  } else if (p.block_table != nullptr) {
+    const Layout pl = w.bnbd ? L_BNSD : L_BSND;
+    FIA_TRY(dense_map(&p.tm_k, &kk, pl, blocks, w.N2, w.bs, w.D));
+    FIA_TRY(dense_map(&p.tm_v, &vv, pl, blocks, w.N2, w.bs, w.D));
+  } else {
+    FIA_TRY(dense_map(&p.tm_k, &kk, w.layout, Bmap, w.N2, rows, w.D));
+    FIA_TRY(dense_map(&p.tm_v, &vv, w.layout, Bmap, w.N2, rows, w.D));
+  }
+  p.tm_qr = p.tm_q;
+  p.tm_kr = p.tm_k;
+  p.rope_col = 128;
+  p.status = make_status(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_check(profiled(s,
+                             [&] {
+                               return launch_prefill_pair(p, int(w.D), int(w.D), query->dtype == FIA_DTYPE_BF16,
+                                                          kWindow, s);
+                             }),
+                    "window prefill launch");
 }
 
 }  // extern "C"

@@ -25,6 +25,12 @@
 // TMEM columns: S_A [0,128), S_B [128,256), O_A [256, 256+DV), O_B [256+DV,
 // 256+2DV).  Causal: tile B needs the K/V tiles of tile A plus at most one; the
 // CTA walks tile B's range and tile A stops early.
+// Window with sinks (kWindow): the band's tiles up to the diagonal, and before
+// them the tiles of the sinks that the band does not hold.  Lengths are read on
+// the device: a CTA finds its batch and rows from its index (TND: by a scan of
+// the running sums), so the launch depends on sizes alone.  Tile B shares tile
+// A's walk, whose first band tile lies before tile B's window: a warp whose
+// rows see nothing of a tile writes P = 0 and skips its softmax.
 // Paged K/V (chunked prefill against a block table): the producer takes each
 // 128-key tile from its block (block_size is a multiple of 128).
 // Explicit mask: a summary pass first gives every 128 x 128 tile of the mask
@@ -113,6 +119,62 @@ __device__ __forceinline__ int tiles_for_rows(const BatchInfo& bi, int qa, int m
   return maxkey >= 0 ? maxkey / kTileN + 1 : 0;
 }
 
+// kWindow: the CTA's item from its index.  CTAs run head by head over one pair
+// of tiles (the heads of a group read the same keys), the last pair of a batch
+// first (it sees most keys).  Every warp does the same scan.  Lengths are taken
+// into their tensors' range, whatever they hold.  False: no rows for this CTA.
+__device__ __forceinline__ bool locate_item(const PrefillParams& p, WorkItem& it, BatchInfo& bi) {
+  const int lane = threadIdx.x & 31;
+  const int x = blockIdx.x / p.num_heads;
+  it.h = blockIdx.x - x * p.num_heads;
+  it.cost = 0;
+  constexpr int kRows = 2 * kTileM;
+  if (!p.is_tnd) {
+    const int nt = (p.s1 + kRows - 1) / kRows;
+    it.b = x / nt;
+    it.q_tile = nt - 1 - (x - it.b * nt);
+    bi.q_start = 0;
+    bi.q_len = p.q_lens == nullptr ? p.s1 : min(max(p.q_lens[it.b], 0), p.s1);
+  } else {
+    int before = 0;
+    it.b = -1;
+    for (int b0 = 0; b0 < p.n_batch; b0 += 32) {
+      const int b = b0 + lane;
+      const int s = b < p.n_batch && b > 0 ? min(max(p.q_lens[b - 1], 0), p.s1) : 0;
+      const int e = b < p.n_batch ? min(max(p.q_lens[b], s), p.s1) : s;
+      const int mine = (e - s + kRows - 1) / kRows;
+      int sum = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, x < before + sum);
+      if (hit != 0u) {
+        const int l = __ffs(hit) - 1;
+        it.b = b0 + l;
+        it.q_tile = __shfl_sync(0xffffffffu, before + sum, l) - 1 - x;
+        bi.q_start = __shfl_sync(0xffffffffu, s, l);
+        bi.q_len = __shfl_sync(0xffffffffu, e - s, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (it.b < 0) return false;
+  }
+  bi.kv_start = 0;
+  if (p.kv_lens == nullptr) {
+    bi.kv_len = p.s2;
+  } else if (p.is_tnd && p.block_table == nullptr) {
+    const int s = it.b > 0 ? min(max(p.kv_lens[it.b - 1], 0), p.s2) : 0;
+    bi.kv_start = s;
+    bi.kv_len = min(max(p.kv_lens[it.b], s), p.s2) - s;
+  } else {
+    bi.kv_len = min(max(p.kv_lens[it.b], 0), p.s2);
+  }
+  return true;
+}
+
 template <int DQK, int DV, bool BF16, int MODE>
 __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_constant__ PrefillParams p) {
   using C = PairCfg<DQK, DV, MODE == kMask>;
@@ -139,8 +201,15 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const WorkItem it = p.items[blockIdx.x];
-  const BatchInfo bi = p.batches[it.b];
+  WorkItem it;
+  BatchInfo bi;
+  if constexpr (MODE == kWindow) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) status_stamp(p.status);   // also when the CTA has no rows
+    if (!locate_item(p, it, bi)) return;
+  } else {
+    it = p.items[blockIdx.x];
+    bi = p.batches[it.b];
+  }
   const int q0 = it.q_tile * 2 * kTileM;
   const int kvh = it.h / p.group;
   const int diag_off = (MODE == kCausal && p.causal_offset_mode == 3) ? (bi.kv_len - bi.q_len) : 0;
@@ -189,10 +258,25 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       nb = has_b ? max(na, lb < 0 ? 0 : lb - first + 1) : 0;
     }
   }
+  // window with sinks: the band's tiles as above with nothing past the
+  // diagonal, n_sink tiles of sinks before them
+  int n_sink = 0;
+  const int64_t win_d = MODE == kWindow ? int64_t(bi.kv_len) - bi.q_len : 0;
+  if (MODE == kWindow) {
+    const int64_t lo = max(int64_t(0), q0 + win_d - p.band_pre);
+    const int64_t hi_a = min(q0 + kTileM, bi.q_len) - 1 + win_d, hi = min(q0 + 2 * kTileM, bi.q_len) - 1 + win_d;
+    jt0 = int(lo / kTileN);
+    const bool rows = q0 < bi.q_len && hi >= 0;   // hi < kv_len, hi >= lo
+    n_sink = rows ? min((p.sink + kTileN - 1) / kTileN, jt0) : 0;
+    na = rows && hi_a >= 0 ? n_sink + int(hi_a / kTileN) - jt0 + 1 : 0;
+    nb = rows && has_b ? n_sink + int(hi / kTileN) - jt0 + 1 : 0;
+  }
+  // K/V tile of the walk's step j
+  auto tile_of = [&](int j) -> int { return MODE == kWindow ? (j < n_sink ? j : jt0 + j - n_sink) : jt0 + j; };
   const int nl = max(na, nb);
 
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) status_stamp(p.status);
+    if (MODE != kWindow && blockIdx.x == 0) status_stamp(p.status);
     mbar_init(q_full, 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
@@ -255,7 +339,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         const int sk = j % KS, sv = j % VS;
         // K/V tile coordinates: (row, batch) of a contiguous tensor, or (row in
         // block, block id) of a paged pool (the table read overlaps the wait)
-        const int key = (jt0 + j) * kTileN;
+        const int key = tile_of(j) * kTileN;
         int kv_r = kv_row0 + key, kv_b = b_coord;
         if (p.block_table != nullptr) {
           kv_b = __ldg(p.block_table + int64_t(it.b) * p.table_stride + key / p.block_size);
@@ -502,6 +586,27 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         warp_arrive(&my_pfull[j & 1]);
         continue;
       }
+      if constexpr (MODE == kWindow) {
+        // the warp's rows see keys up to row 31's position and from row 0's
+        // window or the sinks: a tile outside both has P = 0 (as above)
+        const int kw = tile_of(j) * kTileN;
+        const int64_t p_lo = int64_t(i - lane) + win_d;
+        if (kw > p_lo + 31 || (kw >= p.sink && kw + kTileN - 1 < p_lo - p.band_pre)) {
+          uint32_t z[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[e] = 0u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_off + col_s + c * 16, z);
+          if (kw + kTileN > bi.kv_len && (t == 0 || j >= na) && !clear_v_tail(j, kw)) {
+            ok = false;
+            break;
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&my_pfull[j & 1]);
+          continue;
+        }
+      }
       // S in two halves: the second half's load is in flight while the
       // first half is masked and reduced.
       uint32_t su[4][32];
@@ -512,7 +617,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       tmem_ld32(tmem + lane_off + col_s + 64, su[2]);
       tmem_ld32(tmem + lane_off + col_s + 96, su[3]);
       float* x = reinterpret_cast<float*>(&su[0][0]);
-      const int kv0 = (jt0 + j) * kTileN;
+      const int kv0 = tile_of(j) * kTileN;
       const bool ragged = kv0 + kTileN > bi.kv_len;
       // keys allowed for this row: [lim_lo, lim]
       int lim = (MODE == kCausal) ? min(bi.kv_len - 1, diag) : bi.kv_len - 1;
@@ -522,14 +627,26 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         lim = int(min(int64_t(bi.kv_len) - 1, int64_t(i) + band_d + p.band_next));
         lim_lo = int(max(int64_t(0), int64_t(i) + band_d - p.band_pre));
       }
-      const bool need_mask = ragged || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
+      if (MODE == kWindow) {
+        // keys of the row: [0, sink) and [lim_lo, lim]; in one tile either
+        // part may be empty, so the sinks become an end of their own
+        lim = int(min(int64_t(bi.kv_len) - 1, int64_t(i) + win_d));
+        lim_lo = int(max(int64_t(0), int64_t(i) + win_d - p.band_pre));
+      }
+      const int sink_end = MODE == kWindow ? min(p.sink, lim + 1) : 0;
+      auto hidden = [&](int key) -> bool {
+        if (MODE == kWindow) return key > lim || (key < lim_lo && key >= sink_end);
+        return key > lim || (kBanded && key < lim_lo);
+      };
+      const bool need_mask = (MODE == kWindow && (kv0 + kTileN - 1 > lim || (kv0 < lim_lo && kv0 + kTileN > sink_end))) ||
+                             ragged || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
                              (kBanded && (kv0 + kTileN - 1 > lim || kv0 < lim_lo)) ||
                              (MODE == kMask && (mb[0] | mb[1] | mb[2] | mb[3]) != 0u);
       float a[8];
       if (need_mask) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
-          if (kv0 + c > lim || (kBanded && kv0 + c < lim_lo) || (MODE == kMask && ((mb[c >> 5] >> (c & 31)) & 1u)))
+          if (hidden(kv0 + c) || (MODE == kMask && ((mb[c >> 5] >> (c & 31)) & 1u)))
             su[c >> 5][c & 31] = __float_as_uint(-INFINITY);
       }
 #pragma unroll
@@ -547,7 +664,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       if (need_mask) {
 #pragma unroll
         for (int c = 64; c < 128; ++c)
-          if (kv0 + c > lim || (kBanded && kv0 + c < lim_lo) || (MODE == kMask && ((mb[c >> 5] >> (c & 31)) & 1u)))
+          if (hidden(kv0 + c) || (MODE == kMask && ((mb[c >> 5] >> (c & 31)) & 1u)))
             su[c >> 5][c & 31] = __float_as_uint(-INFINITY);
       }
 #pragma unroll
@@ -621,8 +738,9 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       tc_fence_after();
     }
     if (ok) {
-      const bool row_valid = i < bi.q_len;
-      const bool has = l > 0.f;
+      // (kWindow: the padding rows of a padded layout are this CTA's to write)
+      const bool row_valid = i < (MODE == kWindow && !is_tnd ? p.s1 : bi.q_len);
+      const bool has = MODE == kWindow ? l != 0.f && i < bi.q_len : l > 0.f;
       const float inv_l = has ? 1.f / l : 0.f;
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       T* orow = reinterpret_cast<T*>(p.out) + (is_tnd ? int64_t(bi.q_start + i) * p.out_ss
@@ -695,6 +813,13 @@ cudaError_t launch_mask_tile_summary(const uint8_t* mask, int64_t s1, int64_t s2
 cudaError_t launch_prefill_pair(const PrefillParams& p, int head_dim_qk, int head_dim_v, bool bf16, int mode,
                                 cudaStream_t s) {
   if (p.n_items == 0) return cudaSuccess;
+  if (mode == kWindow) {
+    if (head_dim_qk == 128 && head_dim_v == 128)
+      return bf16 ? launch_pair_one<128, 128, true, kWindow>(p, s) : launch_pair_one<128, 128, false, kWindow>(p, s);
+    if (head_dim_qk == 64 && head_dim_v == 64)
+      return bf16 ? launch_pair_one<64, 64, true, kWindow>(p, s) : launch_pair_one<64, 64, false, kWindow>(p, s);
+    return cudaErrorInvalidValue;
+  }
 #define FIA_PAIR_MODES(DQ, DV, BB)                                          \
   switch (mode) {                                                           \
     case kDense: return launch_pair_one<DQ, DV, BB, kDense>(p, s);          \

@@ -398,6 +398,44 @@ FIA_API fia_status fia_decode_window(const fia_tensor* query, const fia_tensor* 
                              const fia_params* params, int64_t sink_tokens, const fia_tensor* attention_out,
                              const fia_tensor* softmax_lse, void* stream);
 
+/* ------------------------------------------------------------------------
+ * fia_prefill_window: prefill with a sliding window and sink tokens, over
+ * contiguous or paged key/value, with lengths in device memory.  Row i of a
+ * batch has position p = i + kv_len - q_len and sees key j when j <= p and
+ * (j >= p - pre_tokens or j < sink_tokens).
+ *   query, attention_out, softmax_lse: as fia_prefill (BSH / BSND / BNSD /
+ *          TND, f16 or bf16, D 64 or 128).
+ *   key, value: contiguous in the query's layout, or, with block_table, the
+ *          pools of fia_prefill_paged (block_size 128..512, a multiple of 128;
+ *          block ids outside the pool read as zeros; entries of blocks that
+ *          no row sees are never read).
+ *   actual_seq_qlen: device int32 (B); rows of each batch, NULL: S1 for all
+ *          (TND: required, running sums without a leading 0, B <= 4096).
+ *   actual_seq_kvlen: device int32 (B); keys of each batch, NULL: S2 for all
+ *          (paged: required; TND with contiguous keys: required, running sums).
+ *          Values outside what the tensors hold are taken to the nearest
+ *          value inside.  params' own lists must be NULL.
+ *   params->pre_tokens >= 0 (default 2^31-1: causal), sink_tokens >= 0.
+ *          sparse_mode and next_tokens are not read.
+ *   Padding rows of the padded layouts and rows that see no key give 0 and
+ *          +inf; rows of a TND query behind the last sequence stay as they were.
+ *   Values (not scores) of keys that a row does not see enter its sums with a
+ *          weight of 0: they must be finite where they share a 128-key tile with
+ *          a seen key and lie before the batch's length.
+ *   Workspace: the status word.
+ * ------------------------------------------------------------------------ */
+FIA_API fia_status fia_prefill_window_get_workspace_size(const fia_tensor* query, const fia_tensor* key,
+                                                 const fia_tensor* value, const fia_tensor* block_table,
+                                                 const fia_tensor* actual_seq_qlen,
+                                                 const fia_tensor* actual_seq_kvlen, const fia_params* params,
+                                                 int64_t sink_tokens, const fia_tensor* attention_out,
+                                                 const fia_tensor* softmax_lse, size_t* workspace_bytes);
+FIA_API fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor* key, const fia_tensor* value,
+                              const fia_tensor* block_table, const fia_tensor* actual_seq_qlen,
+                              const fia_tensor* actual_seq_kvlen, const fia_params* params, int64_t sink_tokens,
+                              const fia_tensor* attention_out, const fia_tensor* softmax_lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Waits for `stream`, then returns the device-side status recorded in a
  * workspace by the last call that used it (FIA_OK or FIA_ERR_TIMEOUT). */
 FIA_API fia_status fia_device_status(const void* workspace, void* stream);

@@ -262,3 +262,135 @@ def test_window_infinite_values_stay_where_they_are_seen(fia):
                                    pre_tokens=99, sink_tokens=2)
     assert torch.isposinf(out[0, 0, 0, 3]) and torch.isfinite(out[1]).all() and torch.isfinite(out[0, 1]).all()
     assert torch.isfinite(out[0, 0, 0, :3]).all()
+
+
+# ------------------------------------------------------------------ windowed prefill
+def _prefill(fia, ql, kl, n1, n2, D, pre, sink, layout="TND", dt="bf16", bs=0, kv="BNBD", workload=90, pad_q=0, pad_k=0,
+             lens=True, extra_rows=0):
+    """A window prefill against the oracle; returns (out, lse, the case's tensors)."""
+    B, sq, sk = len(ql), max(ql) + pad_q, max(kl) + pad_k
+    norm = fia_inputs.normal
+    scale = D ** -0.5
+    if layout == "TND":
+        q = norm((sum(ql) + extra_rows, n1, D), dt, workload, 1)
+        qs = list(torch.split(q[:sum(ql)], ql))
+        dlq = i32(fia_inputs.cumsum_no_leading_zero(ql))
+    else:
+        q = norm((B, sq, n1, D), dt, workload, 1)
+        qs = [q[b, :ql[b]] for b in range(B)]
+        for b in range(B):
+            q[b, ql[b]:] = float("nan")        # padding rows may hold anything
+        dlq = i32(ql)
+    table = None
+    if bs:
+        c = fia_inputs.paged_decode_case(B, n1, n2, D, kl, block_size=bs, dtype=dt, workload=workload + 1, layout_kv=kv)
+        rows = [tuple(po.cache_rows(f64(x), c.block_table[b], kl[b], n2) for x in (c.k_pool, c.v_pool)) for b in range(B)]
+        k, v, table, dlk = c.k_pool, c.v_pool, c.block_table.clone(), i32(kl)
+        for b in range(B):
+            seen = po.window_see(ql[b], kl[b], pre, sink).any(0) if ql[b] and kl[b] else np.zeros(kl[b], bool)
+            for i in range(-(-kl[b] // bs)):
+                if not seen[i * bs:(i + 1) * bs].any():
+                    table[b, i] = -1 if i % 2 else 10 ** 9   # a block behind every row's window is gone
+    elif layout == "TND":
+        k, v = (norm((sum(kl), n2, D), dt, workload, i) for i in (2, 3))
+        rows = [(f64(a), f64(b)) for a, b in zip(torch.split(k, kl), torch.split(v, kl))]
+        dlk = i32(fia_inputs.cumsum_no_leading_zero(kl))
+    else:
+        k, v = (norm((B, sk, n2, D), dt, workload, i) for i in (2, 3))
+        rows = [(f64(k[b, :kl[b]]), f64(v[b, :kl[b]])) for b in range(B)]
+        for b in range(B):
+            k[b, kl[b]:] = float("nan")
+            v[b, kl[b]:] = float("nan")
+        dlk = i32(kl)
+    lay = {"TND": lambda x: x, "BSND": lambda x: x, "BNSD": lambda x: x.transpose(1, 2).contiguous(),
+           "BSH": lambda x: x.flatten(2)}[layout]
+    qd = lay(q).to(DEV)
+    kd, vd = (x.to(DEV) if bs else lay(x).to(DEV) for x in (k, v))
+    out = torch.full_like(qd, 7.0)
+    lse = torch.full(((q.shape[0], n1, 1) if layout == "TND" else (B, n1, sq, 1)), 7.0, device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    fia.fia_prefill_window(qd, kd, vd, actual_seq_qlen=dlq if lens else None, actual_seq_kvlen=dlk if lens else None,
+                           block_table=None if table is None else table.to(DEV), block_size=bs, num_heads=n1,
+                           num_key_value_heads=n2, scale_value=scale, input_layout=layout, pre_tokens=pre, sink_tokens=sink,
+                           softmax_lse_flag=True, out=out, softmax_lse=lse, workspace=ws)
+    assert fia.fia_device_status(ws) == 0
+    back = {"TND": lambda x: x, "BSND": lambda x: x, "BNSD": lambda x: x.transpose(1, 2),
+            "BSH": lambda x: x.reshape(B, sq, n1, D)}[layout]
+    o, at = back(out), 0
+    for b in range(B):
+        n = ql[b]
+        see = po.window_see(n, kl[b], pre, sink) if kl[b] else np.zeros((n, 0), bool)
+        ref = po.attend(f64(qs[b]), rows[b][0], rows[b][1], see, scale)
+        got = o[at:at + n] if layout == "TND" else o[b, :n]
+        gl = lse[at:at + n, :, 0] if layout == "TND" else lse[b, :, :n, 0].T
+        po.assert_close(got, gl, ref, f"batch {b}")
+        at += n
+        if layout != "TND":
+            assert (o[b, n:] == 0).all() and torch.isposinf(lse[b, :, n:]).all()
+    if layout == "TND":
+        assert (out[sum(ql):] == 7).all() and (lse[sum(ql):] == 7).all()
+    return out, lse, (qd, kd, vd)
+
+
+@pytest.mark.parametrize("pre,sink", [(0, 0), (0, 3), (31, 4), (127, 0), (128, 128), (129, 129), (300, 1), (300, 200), (511, 513),
+                                      (BIG, 0), (100, BIG)])
+def test_prefill_window_masks(fia, pre, sink):
+    _prefill(fia, [1, 700, 128, 0, 257], [1, 700, 128, 0, 257], 4, 2, 128, pre, sink)
+
+
+@pytest.mark.parametrize("layout", ["BNSD", "BSND", "BSH"])
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64), ("bf16", 64)])
+def test_prefill_window_padded(fia, layout, dt, D):
+    """Ragged batches in padded layouts, more keys than rows and fewer; NaN in every padding row."""
+    _prefill(fia, [300, 5, 0, 129], [700, 3, 40, 129], 6, 3, D, 150, 10, layout=layout, dt=dt, pad_q=60, pad_k=9)
+
+
+def test_prefill_window_without_lengths(fia):
+    _prefill(fia, [260, 260], [260, 260], 2, 1, 64, 70, 2, layout="BNSD", dt="f16", lens=False)
+
+
+@pytest.mark.parametrize("bs,kv,layout", [(128, "BNBD", "TND"), (256, "BSH", "TND"), (512, "BNBD", "BNSD"), (128, "BSH", "BSND"),
+                                          (384, "BNBD", "BSH")])
+def test_prefill_window_paged(fia, bs, kv, layout):
+    """Chunks against a cache whose blocks behind the windows are gone from the tables."""
+    _prefill(fia, [200, 1, 300, 64], [1500, 901, 300, 64], 8, 2, 128, 260, 5, layout=layout, bs=bs, kv=kv)
+
+
+def test_prefill_window_many_sequences(fia):
+    """More sequences than a warp scans at once, empty ones among them, rows behind the last one untouched."""
+    r = np.random.default_rng(3)
+    ql = [int(x) for x in r.integers(0, 40, 75)]
+    ql[70] = 600
+    _prefill(fia, ql, ql, 2, 1, 64, 33, 2, extra_rows=37)
+
+
+def test_prefill_window_fewer_keys_than_rows(fia):
+    """Rows before position 0 see nothing, also where a whole 128-row tile lies there."""
+    _prefill(fia, [400, 300], [90, 299], 2, 2, 128, 50, 3)
+
+
+def test_prefill_window_equals_causal(fia):
+    """Without a window: fia_prefill's causal mode, the same bits for one sequence."""
+    ql = [640]
+    out, lse, (q, k, v) = _prefill(fia, ql, ql, 4, 2, 128, BIG, 0)
+    o2, l2 = fia.fia_prefill(q, k, v, num_heads=4, num_key_value_heads=2, scale_value=128 ** -0.5, input_layout="TND",
+                             sparse_mode=3, actual_seq_qlen=ql, actual_seq_kvlen=ql, softmax_lse_flag=True)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_prefill_window_bad_lengths_stay_inside(fia):
+    """Lengths outside the tensors are taken inside: nothing else is read or written."""
+    q, k, v = (fia_inputs.normal((100, 2, 64), "bf16", 97, i).to(DEV) for i in (1, 2, 3))
+    kw = dict(num_heads=2, scale_value=0.125, input_layout="TND", pre_tokens=20, sink_tokens=1)
+    a, _ = fia.fia_prefill_window(q, k, v, actual_seq_qlen=i32([40, 100]), actual_seq_kvlen=i32([40, 100]), **kw)
+    b, _ = fia.fia_prefill_window(q, k, v, actual_seq_qlen=i32([40, 10 ** 9]), actual_seq_kvlen=i32([40, 2 ** 31 - 1]), **kw)
+    assert torch.equal(a, b)
+    fia.fia_prefill_window(q, k, v, actual_seq_qlen=i32([-5, 70]), actual_seq_kvlen=i32([200, 3]), **kw)
+    torch.cuda.synchronize()
+
+
+def test_prefill_window_empty_keys(fia):
+    q = fia_inputs.normal((2, 2, 5, 64), "bf16", 98, 1).to(DEV)
+    k = torch.zeros(2, 2, 0, 64, dtype=torch.bfloat16, device=DEV)
+    out, lse = fia.fia_prefill_window(q, k, k, num_heads=2, input_layout="BNSD", softmax_lse_flag=True)
+    assert (out == 0).all() and torch.isposinf(lse).all()

@@ -183,3 +183,59 @@ def test_oracle_tables_invariants():
         for i in range(new[b]):
             assert slots[at] == tab[b, (ctx[b] + i) // bs] * bs + (ctx[b] + i) % bs
             at += 1
+
+
+# ------------------------------------------------------------------ windowed prefill
+def prefill(lib, layout="TND", T=500, n1=8, n2=2, D=128, B_=3, bs=0, sink=4, prm=None, ws=P, wsb=256, size=False, **kw):
+    p = dict(num_heads=n1, num_key_value_heads=n2, input_layout=layout, block_size=bs, pre_tokens=100)
+    p.update(prm or {})
+    if layout == "TND":
+        q, k = t((T, n1, D)), t((T, n2, D))
+    else:
+        q, k = t((B_, n1, T, D)), t((B_, n2, T, D))
+    if bs:
+        k = t((20, n2, bs, D))
+    a = dict(q=q, k=k, v=k, table=t((B_, 8), I32) if bs else None, ql=t((B_,), I32), kl=t((B_,), I32), out=q, lse=None)
+    a.update(kw)
+    args = [a["q"], a["k"], a["v"], a["table"], a["ql"], a["kl"], ctypes.byref(B.Params(**p).p), sink, a["out"], a["lse"]]
+    n = ctypes.c_size_t(0)
+    r = code(lib.fia_prefill_window_get_workspace_size(*args, ctypes.byref(n)))
+    if size:
+        return r, n.value
+    # the execute call refuses the same
+    return r if r == "FIA_OK" else (r, code(lib.fia_prefill_window(*args, ws, wsb, None)))
+
+
+PREFILL_REFUSALS = [
+    (dict(q=None), "FIA_ERR_NULL"), (dict(v=None), "FIA_ERR_NULL"), (dict(prm=dict(input_layout="NTD")), "FIA_ERR_LAYOUT"),
+    (dict(k=t((500, 2, 128), F16)), "FIA_ERR_DTYPE"), (dict(out=t((500, 8, 128), F16)), "FIA_ERR_DTYPE"),
+    (dict(ql=None), "FIA_ERR_SEQLEN"), (dict(kl=None), "FIA_ERR_SEQLEN"), (dict(ql=t((3,), I64)), "FIA_ERR_DTYPE"),
+    (dict(ql=t((4097,), I32)), "FIA_ERR_SEQLEN"), (dict(kl=t((2,), I32)), "FIA_ERR_SHAPE"), (dict(ql=t((3, 1), I32)), "FIA_ERR_SHAPE"),
+    (dict(prm=dict(actual_seq_qlen=[5])), "FIA_ERR_SEQLEN"), (dict(n1=6, n2=4), "FIA_ERR_HEADS"),
+    (dict(n1=130, n2=2), "FIA_ERR_HEADS"), (dict(D=192), "FIA_ERR_UNSUPPORTED"), (dict(sink=-2), "FIA_ERR_UNSUPPORTED"),
+    (dict(prm=dict(pre_tokens=-3)), "FIA_ERR_UNSUPPORTED"), (dict(prm=dict(scale_value=-1.0)), "FIA_ERR_UNSUPPORTED"),
+    (dict(v=t((400, 2, 128))), "FIA_ERR_SHAPE"), (dict(out=t((500, 4, 128))), "FIA_ERR_SHAPE"),
+    (dict(q=t((500, 8, 128), BF16, P + 4), out=t((500, 8, 128))), "FIA_ERR_ALIGNMENT"),
+    (dict(prm=dict(softmax_lse_flag=True)), "FIA_ERR_NULL"),
+    (dict(prm=dict(softmax_lse_flag=True), lse=t((500, 8, 2), F32)), "FIA_ERR_SHAPE"),
+    (dict(bs=64), "FIA_ERR_BLOCK_TABLE"), (dict(bs=640), "FIA_ERR_BLOCK_TABLE"), (dict(bs=200), "FIA_ERR_BLOCK_TABLE"),
+    (dict(bs=128, table=t((4, 8), I32)), "FIA_ERR_BLOCK_TABLE"), (dict(bs=128, kl=None), "FIA_ERR_SEQLEN"),
+    (dict(bs=128, table=t((3, 0), I32, None)), "FIA_ERR_BLOCK_TABLE"),
+    (dict(bs=128, k=t((20, 4, 128, 128)), v=t((20, 4, 128, 128))), "FIA_ERR_SHAPE"),
+    (dict(layout="BNSD", ql=t((4,), I32)), "FIA_ERR_SHAPE"), (dict(layout="BNSD", k=t((2, 2, 500, 128)), v=t((2, 2, 500, 128))), "FIA_ERR_SHAPE"),
+]
+
+
+@pytest.mark.parametrize("kw,status", PREFILL_REFUSALS)
+def test_prefill_window_refusals(lib, kw, status):
+    assert prefill(lib, **kw) == (status, status)
+
+
+def test_prefill_window_workspace(lib):
+    assert prefill(lib, size=True) == ("FIA_OK", 256)
+    assert prefill(lib, layout="BNSD", ql=None, kl=None, size=True) == ("FIA_OK", 256)
+    q, k = t((500, 8, 128)), t((500, 2, 128))
+    prm = B.Params(num_heads=8, num_key_value_heads=2, input_layout="TND")
+    for ws, n, want in ((None, 256, "FIA_ERR_WORKSPACE"), (P, 255, "FIA_ERR_WORKSPACE"), (P + 8, 256, "FIA_ERR_ALIGNMENT")):
+        r = lib.fia_prefill_window(q, k, k, None, t((3,), I32), t((3,), I32), ctypes.byref(prm.p), 0, q, None, ws, n, None)
+        assert code(r) == want
