@@ -17,13 +17,18 @@ Paged serving, with lengths in device memory:
     fia_prefill_window(query, key, value, actual_seq_qlen=..., pre_tokens=..., sink_tokens=..., ...)
                                          -> (attention_out, softmax_lse)
 
+    fia_decode_shared_prefix(query, key_cache, value_cache, block_table=..., shared_prefix_len=..., ...)
+                                         -> (attention_out, softmax_lse)
+
 The library must have been built (attention_fia_prefill_gb300.build.build());
 there is no CPU path.
 """
 from ._binding import (FIAError, INT32_MAX, bsa_forward, fia_decode, fia_device_status, fia_prefill,  # noqa: F401
                        fia_prefill_mla, fia_prefill_paged, load_library)
-from ._paged import fia_block_table_append, fia_cache_write, fia_decode_window, fia_prefill_window  # noqa: F401
+from ._paged import (fia_block_table_append, fia_cache_write, fia_decode_shared_prefix, fia_decode_window,  # noqa: F401
+                     fia_prefill_window)
 
 __all__ = ["fia_block_table_append", "fia_cache_write", "fia_decode_window", "fia_prefill_window",
+           "fia_decode_shared_prefix",
            "fia_prefill", "fia_prefill_mla", "fia_prefill_paged", "fia_decode", "bsa_forward", "fia_device_status", "FIAError",
            "load_library"]

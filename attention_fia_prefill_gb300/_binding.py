@@ -32,6 +32,7 @@ EXPORTS = [
     "fia_last_error", "fia_profile_next_call", "fia_debug_set_wait_limit_ns", "fia_debug_set_decode_path", "fia_decode_no_alloc",
     "fia_debug_plan_decode", "fia_block_table_append", "fia_cache_write", "fia_decode_window",
     "fia_prefill_window_get_workspace_size", "fia_prefill_window",
+    "fia_decode_shared_prefix_get_workspace_size", "fia_decode_shared_prefix",
 ]
 
 
@@ -131,6 +132,10 @@ def load_library(path: str | None = None):
     lib.fia_prefill_window_get_workspace_size.restype = st
     lib.fia_prefill_window.argtypes = [d, d, d, d, d, d, P, i64, d, d, vp, ctypes.c_size_t, vp]
     lib.fia_prefill_window.restype = st
+    lib.fia_decode_shared_prefix_get_workspace_size.argtypes = [d, d, d, d, d, P, i64, d, d, sz]
+    lib.fia_decode_shared_prefix_get_workspace_size.restype = st
+    lib.fia_decode_shared_prefix.argtypes = [d, d, d, d, d, P, i64, d, d, vp, ctypes.c_size_t, vp]
+    lib.fia_decode_shared_prefix.restype = st
     if path is None:
         _lib = lib
     return lib

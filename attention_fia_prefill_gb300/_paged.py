@@ -166,3 +166,31 @@ def fia_prefill_window(query, key, value, *, actual_seq_qlen=None, actual_seq_kv
             sink_tokens, _desc(out, "out"), _desc(softmax_lse, "softmax_lse"), workspace.data_ptr(), workspace.numel(),
             stream))
     return out, softmax_lse
+
+
+def fia_decode_shared_prefix(query, key_cache, value_cache, *, block_table, block_size, actual_seq_kvlen,
+                             shared_prefix_len, num_heads=1, num_key_value_heads=0, scale_value=1.0, input_layout="BSH",
+                             softmax_lse_flag=False, out=None, softmax_lse=None, workspace=None):
+    """Incremental attention (Q_S 1..16 new tokens) for a batch whose block
+    tables all begin with the blocks of one shared prefix of shared_prefix_len
+    keys (a multiple of block_size), which are read once for the whole batch.
+    actual_seq_kvlen: int32 CUDA tensor (B), whole lengths.  Each token sees the
+    cache up to itself.  Returns (attention_out, softmax_lse or None)."""
+    import torch
+    with _on(query, key_cache, value_cache, block_table, actual_seq_kvlen, out, softmax_lse, workspace) as stream:
+        prm = _params(num_heads=num_heads, num_key_value_heads=num_key_value_heads, scale_value=scale_value,
+                      input_layout=input_layout, block_size=block_size, softmax_lse_flag=softmax_lse_flag)
+        if out is None:
+            out = torch.empty_like(query)
+        if softmax_lse_flag and softmax_lse is None:
+            softmax_lse = query.new_empty(_lse_shape(query, input_layout, num_heads), dtype=torch.float32)
+        lib = load_library()
+        args = (_desc(query, "query"), _desc(key_cache, "key_cache"), _desc(value_cache, "value_cache"),
+                _desc(block_table, "block_table"), _desc(actual_seq_kvlen, "actual_seq_kvlen"), ctypes.byref(prm.p),
+                shared_prefix_len, _desc(out, "out"), _desc(softmax_lse, "softmax_lse"))
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            check(lib.fia_decode_shared_prefix_get_workspace_size(*args, ctypes.byref(n)))
+            workspace = query.new_empty(n.value, dtype=torch.uint8)
+        check(lib.fia_decode_shared_prefix(*args, workspace.data_ptr(), workspace.numel(), stream))
+    return out, softmax_lse

@@ -47,7 +47,9 @@ struct WorkItem {
 // allowed when mask[i][j] == 0 and i - pre <= j <= i + next (mode 1: no band).
 // kWindow: key j of row i allowed when j <= i + d and (j >= i + d - pre or
 // j < sink), d as for kBand; lengths in device memory, no items.
-enum PrefillMode : int { kDense = 0, kCausal = 1, kBlockSparse = 2, kBand = 3, kMask = 4, kWindow = 5 };
+// kPrefix: the rows of a whole decode batch over the keys of its shared prefix,
+// cut into splits that leave partial results.
+enum PrefillMode : int { kDense = 0, kCausal = 1, kBlockSparse = 2, kBand = 3, kMask = 4, kWindow = 5, kPrefix = 6 };
 
 struct PrefillParams {
   // 4-D maps (D, S, N, B); TND uses (D, T, N, 1).  With a paged cache the K/V
@@ -98,6 +100,15 @@ struct PrefillParams {
   const int32_t* q_lens;
   const int32_t* kv_lens;
   int n_batch, s1, s2;            // s1 / s2: rows a batch has (TND: all rows)
+  // kPrefix: tm_q is a 5-D map (D, heads of a group, q_tokens, KV_N, B) whose
+  // box holds the rows of tile_batches sequences; kv_lens the whole lengths;
+  // the prefix's s2 keys lie in the blocks of block_table's first row.
+  // Partial results as SpanParams takes them.
+  int q_tokens, tile_batches, n_pairs, n_splits;
+  int box_rows;                   // min(block_size, 128)
+  float* part_o;
+  float2* part_ml;
+  int64_t part_rows;
 };
 
 // Paged / contiguous decode.  A unit is (batch, kv head).  Every unit's keys

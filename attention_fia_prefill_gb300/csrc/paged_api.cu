@@ -265,6 +265,55 @@ fia_status window_prefill(const fia_tensor* q, const fia_tensor* k, const fia_te
   return FIA_OK;
 }
 
+// How fia_decode_shared_prefix cuts its work.
+struct PrefixPlan {
+  bool split_off = false;   // a kernel for the prefix, joined by the decode of the rest
+  int tile_batches = 0, n_pairs = 0, n_splits = 0;
+  int64_t rows = 0;         // rows of one split's partial results
+  size_t off_ml = 0, bytes = kHeader;
+};
+
+// The prefix kernel's grid: (pairs of 128-row tiles) x kv heads x splits of
+// the prefix's 128-key tiles, one CTA per SM.  The split count is the one
+// whose waves of CTAs take the least time, a CTA costing its tiles and about
+// three more (start, first loads, partial results).
+PrefixPlan prefix_plan(const SpanParams& p, int64_t prefix, int64_t D, int n_sm) {
+  PrefixPlan w;
+  if (prefix == 0 || p.B < 2) return w;   // one sequence shares with nobody
+  w.split_off = true;
+  w.tile_batches = kTileM / p.rows;
+  const int64_t row_tiles = (p.B + w.tile_batches - 1) / w.tile_batches;
+  w.n_pairs = int((row_tiles + 1) / 2);
+  const int64_t per = int64_t(w.n_pairs) * p.N2, tiles = (prefix + kTileN - 1) / kTileN;
+  constexpr int kStart = 3, kMostSplits = 64;
+  int64_t best = 0;
+  for (int s = 1; s <= std::min<int64_t>(tiles, kMostSplits); ++s) {
+    const int64_t cost = (per * s + n_sm - 1) / n_sm * ((tiles + s - 1) / s + kStart);
+    if (w.n_splits == 0 || cost < best) {
+      best = cost;
+      w.n_splits = s;
+    }
+  }
+  w.rows = int64_t(p.B) * p.N1 * p.q_tokens;
+  w.off_ml = kHeader + align_up(size_t(w.n_splits) * size_t(w.rows) * size_t(D) * sizeof(float), 256);
+  w.bytes = w.off_ml + align_up(size_t(w.n_splits) * size_t(w.rows) * sizeof(float2), 256);
+  return w;
+}
+
+fia_status prefix_args(const fia_tensor* q, const fia_tensor* k, const fia_tensor* v, const fia_tensor* table,
+                       const fia_tensor* kvlen, const fia_params* prm, int64_t prefix, const fia_tensor* out,
+                       const fia_tensor* lse, SpanParams& p, int64_t& D) {
+  FIA_TRY(span_params(q, k, v, table, kvlen, prm, out, lse, p, D));
+  if (p.block_table == nullptr) return fail(FIA_ERR_BLOCK_TABLE, "a shared prefix needs block_table");
+  if (p.block_size % 128 != 0 && 128 % p.block_size != 0)
+    return fail(FIA_ERR_BLOCK_TABLE, "block_size %d: a multiple of 16 that divides 128, or a multiple of 128", p.block_size);
+  if (prefix < 0 || prefix > p.kv_max || prefix % p.block_size != 0)
+    return fail(FIA_ERR_SEQLEN, "shared_prefix_len %lld: a multiple of block_size in [0, %d]", (long long)prefix, p.kv_max);
+  p.pre = int(kMaxInt);
+  if (p.n_blocks == 0) p.kv_max = 0;   // an empty pool: no keys
+  return FIA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -414,6 +463,91 @@ fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor* key, co
                                                           kWindow, s);
                              }),
                     "window prefill launch");
+}
+
+fia_status fia_decode_shared_prefix_get_workspace_size(const fia_tensor* query, const fia_tensor* key_cache,
+                                                       const fia_tensor* value_cache, const fia_tensor* block_table,
+                                                       const fia_tensor* actual_seq_kvlen, const fia_params* params,
+                                                       int64_t shared_prefix_len, const fia_tensor* attention_out,
+                                                       const fia_tensor* softmax_lse, size_t* workspace_bytes) {
+  if (workspace_bytes == nullptr) return fail(FIA_ERR_NULL, "workspace_bytes is NULL");
+  *workspace_bytes = kHeader;
+  if (query != nullptr && query->ndim > 0 && numel(query) == 0) return FIA_OK;   // empty query
+  SpanParams p;
+  int64_t D;
+  FIA_TRY(prefix_args(query, key_cache, value_cache, block_table, actual_seq_kvlen, params, shared_prefix_len,
+                      attention_out, softmax_lse, p, D));
+  *workspace_bytes = prefix_plan(p, shared_prefix_len, D, sm_count()).bytes;
+  return FIA_OK;
+}
+
+fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* key_cache,
+                                    const fia_tensor* value_cache, const fia_tensor* block_table,
+                                    const fia_tensor* actual_seq_kvlen, const fia_params* params,
+                                    int64_t shared_prefix_len, const fia_tensor* attention_out,
+                                    const fia_tensor* softmax_lse, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (query != nullptr && query->ndim > 0 && numel(query) == 0) return FIA_OK;
+  SpanParams p;
+  int64_t D;
+  FIA_TRY(prefix_args(query, key_cache, value_cache, block_table, actual_seq_kvlen, params, shared_prefix_len,
+                      attention_out, softmax_lse, p, D));
+  const int n_sm = sm_count();
+  const PrefixPlan w = prefix_plan(p, p.kv_max == 0 ? 0 : shared_prefix_len, D, n_sm);
+  FIA_TRY(check_ws(workspace, workspace_bytes, w.bytes));
+  const bool bf16 = query->dtype == FIA_DTYPE_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  if (!w.split_off) {
+    FIA_TRY(cuda_check(cudaMemsetAsync(base, 0, 8, s), "status reset"));
+    return cuda_check(profiled(s, [&] { return launch_span_decode(p, int(D), bf16, n_sm, s); }), "decode launch");
+  }
+  PrefillParams pp;
+  memset(&pp, 0, sizeof(pp));
+  {
+    // query rows of a (batch, kv head): tokens, and within a token the heads of
+    // the group; one box holds tile_batches sequences
+    const uint64_t e = 2, g = uint64_t(p.group), Q = uint64_t(p.q_tokens);
+    const uint64_t dims[5] = {uint64_t(D), g, Q, uint64_t(p.N2), uint64_t(p.B)};
+    const uint64_t st[4] = {uint64_t(p.q_sn) * e, uint64_t(p.q_ss) * e, uint64_t(p.q_sn) * g * e, uint64_t(p.q_sb) * e};
+    const uint32_t box[5] = {64, uint32_t(g), uint32_t(Q), 1, uint32_t(w.tile_batches)};
+    FIA_TRY(make_map(&pp.tm_q, query->data, 5, dims, st, 0, false, box));
+    // the pools as (D, block_size, KV_N, blocknum)
+    const uint64_t kd[4] = {uint64_t(D), uint64_t(p.block_size), uint64_t(p.N2), uint64_t(p.n_blocks)};
+    const uint64_t ks[3] = {uint64_t(p.row_stride) * e, uint64_t(p.head_stride) * e, uint64_t(p.blk_stride) * e};
+    pp.box_rows = std::min(p.block_size, kTileN);
+    FIA_TRY(make_map(&pp.tm_k, p.k, 4, kd, ks, uint32_t(pp.box_rows)));
+    FIA_TRY(make_map(&pp.tm_v, p.v, 4, kd, ks, uint32_t(pp.box_rows)));
+    pp.tm_qr = pp.tm_q;
+    pp.tm_kr = pp.tm_k;
+  }
+  pp.num_heads = p.N1;
+  pp.num_kv_heads = p.N2;
+  pp.group = p.group;
+  pp.block_table = p.block_table;
+  pp.table_stride = p.table_stride;
+  pp.block_size = p.block_size;
+  pp.scale_log2 = p.scale_log2;
+  pp.kv_lens = p.kv_len;
+  pp.n_batch = p.B;
+  pp.s2 = int(shared_prefix_len);
+  pp.q_tokens = p.q_tokens;
+  pp.tile_batches = w.tile_batches;
+  pp.n_pairs = w.n_pairs;
+  pp.n_splits = w.n_splits;
+  pp.part_o = reinterpret_cast<float*>(base + kHeader);
+  pp.part_ml = reinterpret_cast<float2*>(base + w.off_ml);
+  pp.part_rows = w.rows;
+  pp.n_items = w.n_pairs * p.N2 * w.n_splits;
+  pp.status = make_status(workspace);
+  FIA_TRY(cuda_check(profiled(s, [&] { return launch_prefill_pair(pp, int(D), int(D), bf16, kPrefix, s); }),
+                     "prefix launch"));
+  p.base = int(shared_prefix_len);
+  p.part_o = pp.part_o;
+  p.part_ml = pp.part_ml;
+  p.n_parts = w.n_splits;
+  p.part_rows = w.rows;
+  return cuda_check(launch_span_decode(p, int(D), bf16, n_sm, s), "decode launch");
 }
 
 }  // extern "C"

@@ -31,6 +31,10 @@
 // the running sums), so the launch depends on sizes alone.  Tile B shares tile
 // A's walk, whose first band tile lies before tile B's window: a warp whose
 // rows see nothing of a tile writes P = 0 and skips its softmax.
+// Shared prefix (kPrefix): the rows are a decode batch's, 128 / (heads of a
+// group x new tokens) sequences to a tile, gathered by one 5-D box; the walk is
+// one split of the prefix's tiles (a 128-key tile may take several pages), and
+// the epilogue leaves O, max and sum for the join with each sequence's own keys.
 // Paged K/V (chunked prefill against a block table): the producer takes each
 // 128-key tile from its block (block_size is a multiple of 128).
 // Explicit mask: a summary pass first gives every 128 x 128 tile of the mask
@@ -203,7 +207,19 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WorkItem it;
   BatchInfo bi;
-  if constexpr (MODE == kWindow) {
+  if constexpr (MODE == kPrefix) {
+    grid_dep_launch();   // the decode of the sequences' own keys needs no result of this kernel before its join
+    // splits outermost: the pairs of rows that read the same keys are neighbours
+    const int x = blockIdx.x / p.n_pairs;
+    it.cost = x / p.num_kv_heads;                  // the split
+    it.h = x - it.cost * p.num_kv_heads;           // the kv head
+    it.q_tile = blockIdx.x - x * p.n_pairs;
+    it.b = 0;
+    bi.q_start = bi.kv_start = 0;
+    bi.kv_len = p.s2;
+    // rows in tile space: every tile has 128
+    bi.q_len = ((p.n_batch + p.tile_batches - 1) / p.tile_batches) * kTileM;
+  } else if constexpr (MODE == kWindow) {
     if (threadIdx.x == 0 && blockIdx.x == 0) status_stamp(p.status);   // also when the CTA has no rows
     if (!locate_item(p, it, bi)) return;
   } else {
@@ -211,7 +227,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
     bi = p.batches[it.b];
   }
   const int q0 = it.q_tile * 2 * kTileM;
-  const int kvh = it.h / p.group;
+  const int kvh = MODE == kPrefix ? it.h : it.h / p.group;
   const int diag_off = (MODE == kCausal && p.causal_offset_mode == 3) ? (bi.kv_len - bi.q_len) : 0;
   int na = tiles_for_rows(bi, q0, MODE, diag_off);
   // Tile B walks at least tile A's range (its rows past the batch are computed
@@ -271,6 +287,12 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
     na = rows && hi_a >= 0 ? n_sink + int(hi_a / kTileN) - jt0 + 1 : 0;
     nb = rows && has_b ? n_sink + int(hi / kTileN) - jt0 + 1 : 0;
   }
+  if (MODE == kPrefix) {
+    const int tiles = (p.s2 + kTileN - 1) / kTileN;
+    jt0 = int(int64_t(tiles) * it.cost / p.n_splits);
+    na = int(int64_t(tiles) * (it.cost + 1) / p.n_splits) - jt0;
+    nb = has_b ? na : 0;
+  }
   // K/V tile of the walk's step j
   auto tile_of = [&](int j) -> int { return MODE == kWindow ? (j < n_sink ? j : jt0 + j - n_sink) : jt0 + j; };
   const int nl = max(na, nb);
@@ -322,6 +344,15 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         col = c < 2 ? c * 64 : p.rope_col;
         return c < 2 ? m : mr;
       };
+      if constexpr (MODE == kPrefix) {
+        // (boxes past the batch are filled with zeros and count in full)
+        const int rows = p.tile_batches * p.group * p.q_tokens;
+        mbar_arrive_expect_tx(q_full, 2 * C::kChunksQK * rows * 128);
+        for (int t = 0; t < 2; ++t)
+          for (int c = 0; c < C::kChunksQK; ++c)
+            tma_load_5d(smem + C::kOffQ + t * C::kTileQK + c * C::kBoxBytes, &p.tm_q, q_full, c * 64, 0, 0, kvh,
+                        (2 * it.q_tile + t) * p.tile_batches);
+      } else {
       mbar_arrive_expect_tx(q_full, 2 * C::kTileQK);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -332,6 +363,17 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
           tma_load_4d(smem + C::kOffQ + t * C::kTileQK + c * C::kBoxBytes, m, q_full, col, q_row0 + t * kTileM, it.h,
                       b_coord);
         }
+      }
+      // one 128-key tile of a paged prefix, page by page (a page id outside
+      // the pool, or past the prefix, reads as zeros)
+      auto prefix_tile = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int key) {
+        for (int r = 0; r < kTileN; r += p.box_rows) {
+          const int k = key + r;
+          const int id = k < p.s2 ? p.block_table[k / p.block_size] : -1;
+          for (int c = 0; c < DV / 64; ++c)
+            tma_load_4d(dst + c * C::kBoxBytes + r * 128, m, bar, c * 64, k % p.block_size, kvh, id);
+        }
+      };
       // the Q K^T that frees a K stage: tile B's, or tile A's without a tile B
       uint64_t* k_rel = s_full + (nb > 0 ? 3 : 0);
       int j = 0, nk = 0, nv = 0;   // tiles loaded; K and V loads issued
@@ -341,15 +383,16 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         // block, block id) of a paged pool (the table read overlaps the wait)
         const int key = tile_of(j) * kTileN;
         int kv_r = kv_row0 + key, kv_b = b_coord;
-        if (p.block_table != nullptr) {
+        if (MODE != kPrefix && p.block_table != nullptr) {
           kv_b = __ldg(p.block_table + int64_t(it.b) * p.table_stride + key / p.block_size);
           kv_r = key % p.block_size;
         }
         if (j >= KS && !mbar_wait_lean(&k_rel[sk], ((j / KS) - 1) & 1, abort_flag, p.status)) break;
         uint8_t* ks = smem + C::kOffK + sk * C::kTileQK;
         mbar_arrive_expect_tx(&k_full[sk], C::kTileQK);
+        if constexpr (MODE == kPrefix) prefix_tile(ks, &p.tm_k, &k_full[sk], key);
 #pragma unroll
-        for (int c = 0; c < C::kChunksQK; ++c) {
+        for (int c = 0; c < (MODE == kPrefix ? 0 : C::kChunksQK); ++c) {
           int col;
           const CUtensorMap* m = qk_src(c, &p.tm_k, &p.tm_kr, col);
           tma_load_4d(ks + c * C::kBoxBytes, m, &k_full[sk], col, kv_r, kvh, kv_b);
@@ -358,8 +401,9 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         if (j >= VS && !mbar_wait_lean(&v_free[sv], ((j / VS) - 1) & 1, abort_flag, p.status)) break;
         uint8_t* vs = smem + C::kOffV + sv * C::kTileV;
         mbar_arrive_expect_tx(&v_full[sv], C::kTileV);
+        if constexpr (MODE == kPrefix) prefix_tile(vs, &p.tm_v, &v_full[sv], key);
 #pragma unroll
-        for (int c = 0; c < C::kChunksV; ++c)
+        for (int c = 0; c < (MODE == kPrefix ? 0 : C::kChunksV); ++c)
           tma_load_4d(vs + c * C::kBoxBytes, &p.tm_v, &v_full[sv], c * 64, kv_r, kvh, kv_b);
         nv = j + 1;
         if (j == 0 && p.prefetch_stride > 0 && int(blockIdx.x) + p.prefetch_stride < p.n_items) {
@@ -538,6 +582,18 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       fence_proxy_async_smem();
       return true;
     };
+    // kPrefix: this row's sequence, head of the group and token, and the end of
+    // the prefix's keys that it sees (the whole prefix, but for a sequence
+    // shorter than it)
+    int pb = 0, ph = 0, pt = 0, p_end = 0;
+    if constexpr (MODE == kPrefix) {
+      const int unit_rows = p.group * p.q_tokens;
+      pb = r < p.tile_batches * unit_rows ? (2 * it.q_tile + t) * p.tile_batches + r / unit_rows : p.n_batch;
+      pt = (r % unit_rows) / p.group;
+      ph = r % p.group;
+      if (pb < p.n_batch) p_end = min(max(max(p.kv_lens[pb], 0) - p.q_tokens + pt + 1, 0), p.s2);
+    }
+    const bool warp_rows = MODE != kPrefix || __any_sync(0xffffffffu, pb < p.n_batch);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -567,6 +623,12 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         break;
       }
       tc_fence_after();
+      if (MODE == kPrefix && !warp_rows) {
+        // no row of this warp is anybody's: whatever S holds serves as P
+        tc_fence_before();
+        warp_arrive(&my_pfull[j & 1]);
+        continue;
+      }
       if (MODE == kMask && __all_sync(0xffffffffu, (mb[0] & mb[1] & mb[2] & mb[3]) == 0xffffffffu)) {
         // the mask hides every key of this tile from all of the warp's rows:
         // P = 0, and the max, the sum and O stay as they are (what the full
@@ -635,11 +697,13 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       }
       const int sink_end = MODE == kWindow ? min(p.sink, lim + 1) : 0;
       auto hidden = [&](int key) -> bool {
+        if (MODE == kPrefix) return key >= p_end;
         if (MODE == kWindow) return key > lim || (key < lim_lo && key >= sink_end);
         return key > lim || (kBanded && key < lim_lo);
       };
-      const bool need_mask = (MODE == kWindow && (kv0 + kTileN - 1 > lim || (kv0 < lim_lo && kv0 + kTileN > sink_end))) ||
-                             ragged || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
+      const bool need_mask = (MODE == kPrefix && kv0 + kTileN > p_end) ||
+                             (MODE == kWindow && (kv0 + kTileN - 1 > lim || (kv0 < lim_lo && kv0 + kTileN > sink_end))) ||
+                             (MODE != kPrefix && ragged) || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
                              (kBanded && (kv0 + kTileN - 1 > lim || kv0 < lim_lo)) ||
                              (MODE == kMask && (mb[0] | mb[1] | mb[2] | mb[3]) != 0u);
       float a[8];
@@ -719,7 +783,8 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
           tmem_st16(tmem + lane_off + col_o + c * 16, u);
         }
       }
-      if (ragged && (t == 0 || j >= na) && !clear_v_tail(j, kv0)) {
+      // (a prefix ends with a page, and what follows in its tile is zeros)
+      if (MODE != kPrefix && ragged && (t == 0 || j >= na) && !clear_v_tail(j, kv0)) {
         ok = false;
         break;
       }
@@ -737,7 +802,25 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
                                        : mbar_wait_lean(&v_free[jl % VS], (jl / VS) & 1, abort_flag, p.status));
       tc_fence_after();
     }
-    if (ok) {
+    if (MODE == kPrefix) {
+      // a warp of live rows: O as it is, with its max and sum
+      if (ok && warp_rows) {
+        const int64_t row = (int64_t(pb) * p.num_heads + kvh * p.group + ph) * p.q_tokens + pt + it.cost * p.part_rows;
+        const bool live = pb < p.n_batch;
+        if (live) p.part_ml[row] = make_float2(m, l);
+#pragma unroll
+        for (int c = 0; c < DV / 32; ++c) {
+          uint32_t u[32];
+          tmem_ld32(tmem + lane_off + col_o + c * 32, u);
+          tmem_wait_ld(u);
+          if (live)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(p.part_o + row * DV + c * 32 + q * 4) =
+                  make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+        }
+      }
+    } else if (ok) {
       // (kWindow: the padding rows of a padded layout are this CTA's to write)
       const bool row_valid = i < (MODE == kWindow && !is_tnd ? p.s1 : bi.q_len);
       const bool has = MODE == kWindow ? l != 0.f && i < bi.q_len : l > 0.f;
@@ -818,6 +901,13 @@ cudaError_t launch_prefill_pair(const PrefillParams& p, int head_dim_qk, int hea
       return bf16 ? launch_pair_one<128, 128, true, kWindow>(p, s) : launch_pair_one<128, 128, false, kWindow>(p, s);
     if (head_dim_qk == 64 && head_dim_v == 64)
       return bf16 ? launch_pair_one<64, 64, true, kWindow>(p, s) : launch_pair_one<64, 64, false, kWindow>(p, s);
+    return cudaErrorInvalidValue;
+  }
+  if (mode == kPrefix) {
+    if (head_dim_qk == 128 && head_dim_v == 128)
+      return bf16 ? launch_pair_one<128, 128, true, kPrefix>(p, s) : launch_pair_one<128, 128, false, kPrefix>(p, s);
+    if (head_dim_qk == 64 && head_dim_v == 64)
+      return bf16 ? launch_pair_one<64, 64, true, kPrefix>(p, s) : launch_pair_one<64, 64, false, kPrefix>(p, s);
     return cudaErrorInvalidValue;
   }
 #define FIA_PAIR_MODES(DQ, DV, BB)                                          \

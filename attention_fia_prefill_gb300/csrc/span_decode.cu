@@ -135,7 +135,9 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   const int b = unit / p.N2, kvh = unit - b * p.N2;
 
   grid_dep_launch();
-  grid_dep_wait();
+  // Behind a prefix kernel (an ordinary launch, so everything before it is
+  // complete) only the join has to wait for it.
+  if (p.n_parts == 0) grid_dep_wait();
 
   const int L = p.kv_len == nullptr ? p.kv_max : min(max(p.kv_len[b], 0), p.kv_max);
   const int first = L - p.q_tokens;               // position of token 0 (may be negative: tokens that see nothing)
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     }
     cluster_sync_all();
   }
+  if (p.n_parts > 0) grid_dep_wait();
   const int n_own = cs > 1 ? int(cs) : C::kGroups;
   const uint32_t ob_a = smem_u32(ob), ml_a = smem_u32(ml);
   for (int e = int(rank) * kSpanThreads + threadIdx.x; e < items; e += int(cs) * kSpanThreads) {
@@ -382,6 +385,7 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     };
     float top = -INFINITY;
     for (int g = 0; g < n_own; ++g) top = fmaxf(top, own_ml(g).x);
+#pragma unroll 4
     for (int g = 0; g < p.n_parts; ++g) top = fmaxf(top, p.part_ml[g * p.part_rows + prow].x);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
@@ -393,10 +397,12 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
       l += w * x.y;
       a.x += w * y.x; a.y += w * y.y; a.z += w * y.z; a.w += w * y.w;
     }
+#pragma unroll 4
     for (int g = 0; g < p.n_parts; ++g) {
       const float2 x = p.part_ml[g * p.part_rows + prow];
       const float w = join_weight(x.x, top);
-      const float4 y = *reinterpret_cast<const float4*>(p.part_o + (g * p.part_rows + prow) * D + c4 * 4);
+      float4 y = *reinterpret_cast<const float4*>(p.part_o + (g * p.part_rows + prow) * D + c4 * 4);
+      if (x.x == -INFINITY) y = make_float4(0.f, 0.f, 0.f, 0.f);   // an empty part's O may be 0 * NaN
       l += w * x.y;
       a.x += w * y.x; a.y += w * y.y; a.z += w * y.z; a.w += w * y.w;
     }

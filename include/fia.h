@@ -436,6 +436,33 @@ FIA_API fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor*
                               const fia_tensor* attention_out, const fia_tensor* softmax_lse, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * fia_decode_shared_prefix: incremental attention for a batch whose sequences
+ * begin with the same keys.  The result is fia_decode_window's without a
+ * window; the prefix's keys and values are read once for the whole batch.
+ *   query, key_cache, value_cache, block_table, actual_seq_kvlen (the whole
+ *          lengths, prefix and new tokens among them), attention_out,
+ *          softmax_lse: as fia_decode_window with paged key/value;
+ *          block_size a multiple of 16 that divides 128, or a multiple of 128.
+ *   shared_prefix_len: a multiple of block_size, at most the keys of the
+ *          table's columns.  The first shared_prefix_len / block_size entries
+ *          of every row of block_table must be the same; the first row's are
+ *          read.  A sequence shorter than the prefix sees its own length's keys
+ *          of it (values of the others must be finite).
+ *   Workspace: the status word and the prefix's partial results.
+ * ------------------------------------------------------------------------ */
+FIA_API fia_status fia_decode_shared_prefix_get_workspace_size(const fia_tensor* query, const fia_tensor* key_cache,
+                                                       const fia_tensor* value_cache, const fia_tensor* block_table,
+                                                       const fia_tensor* actual_seq_kvlen, const fia_params* params,
+                                                       int64_t shared_prefix_len, const fia_tensor* attention_out,
+                                                       const fia_tensor* softmax_lse, size_t* workspace_bytes);
+FIA_API fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* key_cache,
+                                    const fia_tensor* value_cache, const fia_tensor* block_table,
+                                    const fia_tensor* actual_seq_kvlen, const fia_params* params,
+                                    int64_t shared_prefix_len, const fia_tensor* attention_out,
+                                    const fia_tensor* softmax_lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
 /* Waits for `stream`, then returns the device-side status recorded in a
  * workspace by the last call that used it (FIA_OK or FIA_ERR_TIMEOUT). */
 FIA_API fia_status fia_device_status(const void* workspace, void* stream);

@@ -394,3 +394,85 @@ def test_prefill_window_empty_keys(fia):
     k = torch.zeros(2, 2, 0, 64, dtype=torch.bfloat16, device=DEV)
     out, lse = fia.fia_prefill_window(q, k, k, num_heads=2, input_layout="BNSD", softmax_lse_flag=True)
     assert (out == 0).all() and torch.isposinf(lse).all()
+
+
+# ------------------------------------------------------------------ shared prefix
+def _prefix(fia, own_lens, P, n1, n2, D, Q=1, bs=128, dt="bf16", kv="BNBD", layout="BNSD", workload=100, totals=None):
+    """own_lens: keys of each sequence behind the prefix; totals overrides whole lengths (sequences shorter than it)."""
+    B, scale = len(own_lens), D ** -0.5
+    lens = [P + n for n in own_lens] if totals is None else totals
+    pages = P // bs
+    c = fia_inputs.paged_decode_case(B, n1, n2, D, own_lens, block_size=bs, dtype=dt, workload=workload, layout_kv=kv,
+                                     q_tokens=Q)
+    r = np.random.default_rng(P + B)
+    first = c.k_pool.shape[0] + r.permutation(pages)
+    shape = (pages,) + tuple(c.k_pool.shape[1:])
+    kp, vp = (torch.cat([x, fia_inputs.normal(shape, dt, workload, i)]) for i, x in ((7, c.k_pool), (8, c.v_pool)))
+    table = torch.cat([torch.tensor(first, dtype=torch.int32).expand(B, pages), c.block_table], 1).contiguous()
+    q = c.q if layout == "BNSD" else c.q.transpose(1, 2).contiguous()
+    q = q.flatten(2) if layout == "BSH" else q
+    kw = dict(block_table=table.to(DEV), block_size=bs, actual_seq_kvlen=i32(lens), num_heads=n1, num_key_value_heads=n2,
+              scale_value=scale, input_layout=layout, softmax_lse_flag=True)
+    args = [x.to(DEV) for x in (q, kp, vp)]
+    out, lse = fia.fia_decode_shared_prefix(*args, shared_prefix_len=P, **kw)
+    torch.cuda.synchronize()
+    o = out.reshape(B, Q, n1, D).transpose(1, 2) if layout != "BNSD" else out
+    pf, vf = f64(kp), f64(vp)
+    rows = [tuple(po.cache_rows(x, table[b], lens[b], n2) for x in (pf, vf)) for b in range(B)]
+    po.assert_close(o, lse, po.decode(c.q, rows, lens, 1 << 40, 0, scale))
+    again, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=P, **kw)
+    assert torch.equal(out, again)
+    return out, lse, args, kw
+
+
+@pytest.mark.parametrize("P", [128, 256, 384, 1152, 4096])
+@pytest.mark.parametrize("B", [2, 5, 40])
+def test_prefix_lengths(fia, P, B):
+    _prefix(fia, [(i * 37) % 200 + 1 for i in range(B)], P, 8, 2, 128)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 256])
+@pytest.mark.parametrize("kv", ["BNBD", "BSH"])
+def test_prefix_pages(fia, bs, kv):
+    """Pages below a tile, prefixes that end inside one."""
+    _prefix(fia, [1, bs, 3 * bs + 1], bs * (7 if bs < 128 else 3), 8, 2, 128, bs=bs, kv=kv, workload=101 + bs)
+
+
+@pytest.mark.parametrize("n1,n2,Q,B", [(4, 4, 1, 300), (32, 8, 1, 33), (7, 1, 1, 40), (28, 4, 2, 12), (16, 1, 4, 5), (64, 1, 1, 3),
+                                       (3, 3, 16, 20), (5, 1, 3, 9), (40, 8, 1, 26), (8, 8, 1, 130)])
+def test_prefix_rows(fia, n1, n2, Q, B):
+    """Row tiles of 128 / (heads x tokens) sequences: whole, part-filled, one to many tiles, odd groups."""
+    _prefix(fia, [Q + (i * 13) % 60 for i in range(B)], 640, n1, n2, 64, Q=Q, bs=64, workload=103 + n1)
+
+
+@pytest.mark.parametrize("dt,D", [("f16", 128), ("bf16", 64), ("f16", 64)])
+@pytest.mark.parametrize("layout", ["BSND", "BSH"])
+def test_prefix_types_and_layouts(fia, dt, D, layout):
+    _prefix(fia, [3, 70, 40], 512, 8, 2, D, Q=3, dt=dt, layout=layout)
+
+
+def test_prefix_short_and_empty_sequences(fia):
+    """Lengths inside the prefix, at its end, zero and below the number of new tokens."""
+    _prefix(fia, [1, 1, 1, 1, 1, 50], 256, 4, 2, 128, Q=2, totals=[0, 1, 100, 256, 257, 306])
+
+
+def test_prefix_without_prefix_and_single_sequence(fia):
+    out, lse, args, kw = _prefix(fia, [40, 300], 0, 8, 2, 128)
+    w, l2 = fia.fia_decode_window(*args, **kw)
+    assert torch.equal(out, w) and torch.equal(lse, l2)
+    _prefix(fia, [77], 512, 8, 2, 128)
+
+
+def test_prefix_reads_the_first_row_only(fia):
+    """The prefix comes from the table's first row: other rows' entries of it are not looked at."""
+    out, _, args, kw = _prefix(fia, [9, 30, 200], 384, 8, 2, 128)
+    kw["block_table"][1:, :3] = -9
+    o2, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=384, **kw)
+    assert torch.equal(out, o2)
+
+
+def test_prefix_status_and_workspace(fia):
+    out, _, args, kw = _prefix(fia, [9, 30, 200], 384, 8, 2, 128)
+    ws = torch.full((1 << 24,), 255, dtype=torch.uint8, device=DEV)
+    o2, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=384, workspace=ws, **kw)
+    assert torch.equal(out, o2) and fia.fia_device_status(ws) == 0

@@ -239,3 +239,41 @@ def test_prefill_window_workspace(lib):
     for ws, n, want in ((None, 256, "FIA_ERR_WORKSPACE"), (P, 255, "FIA_ERR_WORKSPACE"), (P + 8, 256, "FIA_ERR_ALIGNMENT")):
         r = lib.fia_prefill_window(q, k, k, None, t((3,), I32), t((3,), I32), ctypes.byref(prm.p), 0, q, None, ws, n, None)
         assert code(r) == want
+
+
+# ------------------------------------------------------------------ shared prefix
+def prefix(lib, B_=4, n1=8, n2=2, Q=1, D=128, nb=40, bs=128, cols=8, P_len=512, prm=None, ws=P, wsb=1 << 30, **kw):
+    p = dict(num_heads=n1, num_key_value_heads=n2, input_layout="BNSD", block_size=bs)
+    p.update(prm or {})
+    q = t((B_, n1, Q, D))
+    a = dict(q=q, k=t((nb, n2, bs, D)), v=t((nb, n2, bs, D)), table=t((B_, cols), I32), lens=t((B_,), I32), out=q, lse=None)
+    a.update(kw)
+    args = [a["q"], a["k"], a["v"], a["table"], a["lens"], ctypes.byref(B.Params(**p).p), P_len, a["out"], a["lse"]]
+    n = ctypes.c_size_t(0)
+    r = code(lib.fia_decode_shared_prefix_get_workspace_size(*args, ctypes.byref(n)))
+    return (r, n.value) if r == "FIA_OK" else (r, code(lib.fia_decode_shared_prefix(*args, ws, wsb, None)))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(table=None), "FIA_ERR_SHAPE"), (dict(table=None, k=t((4, 2, 128, 128)), v=t((4, 2, 128, 128))), "FIA_ERR_BLOCK_TABLE"),
+    (dict(P_len=100), "FIA_ERR_SEQLEN"), (dict(P_len=-128), "FIA_ERR_SEQLEN"), (dict(P_len=8 * 128 + 128), "FIA_ERR_SEQLEN"),
+    (dict(bs=48, P_len=48), "FIA_ERR_BLOCK_TABLE"), (dict(bs=192, P_len=192), "FIA_ERR_BLOCK_TABLE"), (dict(lens=None), "FIA_ERR_SEQLEN"),
+    (dict(q=None), "FIA_ERR_NULL"), (dict(D=192), "FIA_ERR_UNSUPPORTED"), (dict(n1=48, n2=1, Q=2), "FIA_ERR_UNSUPPORTED"),
+    (dict(prm=dict(input_layout="TND")), "FIA_ERR_UNSUPPORTED"), (dict(v=t((40, 2, 64, 128))), "FIA_ERR_SHAPE"),
+    (dict(k=t((40, 2, 128, 128), F16)), "FIA_ERR_DTYPE"), (dict(prm=dict(actual_seq_kvlen=[9])), "FIA_ERR_SEQLEN"),
+])
+def test_prefix_refusals(lib, kw, status):
+    assert prefix(lib, **kw) == (status, status)
+
+
+def test_prefix_workspace(lib):
+    """One sequence, or no prefix: the status word; else whole splits of fp32 rows."""
+    assert prefix(lib, B_=1) == ("FIA_OK", 256) and prefix(lib, P_len=0) == ("FIA_OK", 256)
+    r, n = prefix(lib)
+    one = 4 * 8 * (128 * 4 + 8)
+    assert r == "FIA_OK" and n > 256 and 1 <= (n - 256) / one <= 4.1
+    q, k = t((4, 8, 1, 128)), t((40, 2, 128, 128))
+    prm = B.Params(num_heads=8, num_key_value_heads=2, input_layout="BNSD", block_size=128)
+    for ws, have, want in ((None, n, "FIA_ERR_WORKSPACE"), (P, 256, "FIA_ERR_WORKSPACE"), (P + 8, n, "FIA_ERR_ALIGNMENT")):
+        assert code(lib.fia_decode_shared_prefix(q, k, k, t((4, 8), I32), t((4,), I32), ctypes.byref(prm.p), 512, q, None, ws,
+                                                 have, None)) == want
