@@ -120,7 +120,8 @@ def load_library(path: str | None = None):
     lib.fia_debug_plan_decode.argtypes = [i32p, ctypes.c_int, ctypes.c_int, ctypes.c_int, i32p, ctypes.c_int, i32p,
                                           ctypes.c_int, i32p, ctypes.c_int, ip, ip]
     lib.fia_debug_plan_decode.restype = st
-    # the paged-serving operators (_paged.py) pass packed descriptors as byte strings
+    # the paged-serving operators, for callers without torch (descriptors as byte strings); _paged.py has a compiled
+    # binding of its own
     d, i64 = ctypes.c_char_p, ctypes.c_int64
     lib.fia_block_table_append.argtypes = [d, d, d, i64, d, d, d, d, d, vp]
     lib.fia_block_table_append.restype = st

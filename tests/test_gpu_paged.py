@@ -476,3 +476,34 @@ def test_prefix_status_and_workspace(fia):
     ws = torch.full((1 << 24,), 255, dtype=torch.uint8, device=DEV)
     o2, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=384, workspace=ws, **kw)
     assert torch.equal(out, o2) and fia.fia_device_status(ws) == 0
+
+
+# ------------------------------------------------------------------ the binding
+def test_binding_checks(fia):
+    """What the binding refuses, and the library's refusals as FIAError with the status."""
+    q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(2, 2, 50, 64, dtype=torch.bfloat16, device=DEV)
+    kw = dict(num_heads=4, num_key_value_heads=2, input_layout="BNSD")
+    with pytest.raises(ValueError, match="contiguous"):
+        fia.fia_decode_window(q, k.transpose(2, 3), k, **kw)
+    with pytest.raises(ValueError, match="CUDA"):
+        fia.fia_decode_window(q, k.cpu(), k, **kw)
+    with pytest.raises(TypeError, match="tensor"):
+        fia.fia_decode_window(q, k, k, actual_seq_kvlen=[3, 4], **kw)
+    with pytest.raises(TypeError, match="dtype"):
+        fia.fia_decode_window(q.double(), k, k, **kw)
+    with pytest.raises(fia.FIAError) as e:
+        fia.fia_decode_window(q, k, k, pre_tokens=-1, **kw)
+    assert e.value.status == 5 and "pre_tokens" in str(e.value)
+    with pytest.raises(fia.FIAError):
+        fia.fia_decode_window(q, k, k, actual_seq_kvlen=torch.zeros(2, dtype=torch.int64, device=DEV), **kw)
+    with pytest.raises(ValueError, match="contiguous"):
+        x = torch.zeros(4, 64, 2, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
+        fia.fia_cache_write(x, None, k, None, i32([0, 1, 2, 3]))
+    z = i32([1, 2])
+    with pytest.raises(ValueError, match="num_tokens"):
+        fia.fia_block_table_append(z, z.clone(), z.clone(), torch.zeros(2, 2, dtype=torch.int32, device=DEV), block_size=4,
+                                   num_tokens=5, slot_mapping=i32([0, 0]))
+    with pytest.raises(fia.FIAError, match="overlap"):
+        fia.fia_block_table_append(z, z.clone(), z.clone(), torch.zeros(2, 2, dtype=torch.int32, device=DEV), block_size=4,
+                                   num_tokens=5, kv_lens=z)

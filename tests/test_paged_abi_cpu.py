@@ -128,14 +128,14 @@ def test_window_empty_query(lib):
 
 
 # ------------------------------------------------------------------ the binding's own checks
-def test_binding_refuses_before_the_library():
+def test_binding_refuses_before_the_library(lib):
     torch = pytest.importorskip("torch")
     import attention_fia_prefill_gb300 as fia
     x = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         fia.fia_block_table_append(x, x, x, torch.zeros(4, 2, dtype=torch.int32), block_size=16, num_tokens=4)
-    with pytest.raises(TypeError, match="int32"):
-        fia.fia_block_table_append(x.long(), x, x, x, block_size=16, num_tokens=4)
+    with pytest.raises(TypeError, match="tensor"):
+        fia.fia_block_table_append([1, 2], x, x, x, block_size=16, num_tokens=4)
     k = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         fia.fia_cache_write(k, k, k, k, x)
