@@ -25,7 +25,9 @@
 //     a step, relative, of each weight), its sum is not rounded.
 //   * Join: the groups' (O, max, sum) meet in shared memory, the CTAs' over
 //     distributed shared memory, with the exact weights 2^(m - max m): one
-//     launch, no workspace, no atomics, the same bits on every run.
+//     launch, no workspace, no atomics, the same bits on every run.  Each CTA
+//     sends its results to the CTA that writes them (one barrier; reading them
+//     there took a second one, so that no CTA left while it was read: 1.5 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -37,18 +39,25 @@ namespace {
 
 constexpr int kSpanThreads = 128;
 constexpr int kSpanTile = 16;        // keys of a tile
+constexpr int kMostCtas = 8;         // CTAs of a unit (a portable cluster)
 
 template <int D, int MT>
 struct SpanCfg {
   static constexpr int kGroups = 4 / MT;
-  static constexpr int kStages = 3 * MT;                  // per group: the same bytes in flight for every MT
+  // per group; about the same bytes in flight for every MT, two CTAs per SM
+  static constexpr int kStages = MT == 1 ? 3 : MT == 2 ? 5 : 8;
   static constexpr int kTileBytes = kSpanTile * D * 2;    // K or V
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kRing = kGroups * kStages * kStageBytes;
-  // after the loop: O of every group [kGroups][16 MT][D] and (max, sum)
-  static constexpr int kOffML = kGroups * 16 * MT * D * 4;
-  static constexpr int kMerge = kOffML + kGroups * 16 * MT * 8;
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 128;
+  // after the loop the rings hold O of every group [kGroups][16 MT][D]
+  static constexpr int kO = kGroups * 16 * MT * D * 4;
+  static_assert(kO <= kRing, "the groups' results take the rings' place");
+  // (max, sum) of every group; results of the cluster's CTAs for this CTA's
+  // share of the unit's float4s, and their (max, sum) of every row
+  static constexpr int kOffML = kRing;
+  static constexpr int kOffIn = kOffML + kGroups * 16 * MT * 8;
+  static constexpr int kOffInML = kOffIn + (16 * MT * (D / 4) + kMostCtas) * 16;
+  static constexpr int kSmem = kOffInML + kMostCtas * 16 * MT * 8 + 128;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -91,26 +100,21 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// The cluster's barrier in halves: arrive releases this thread's writes, wait
+// acquires every CTA's.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t peer_addr(uint32_t smem, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
   return a;
 }
-__device__ __forceinline__ float4 ld_peer4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
+__device__ __forceinline__ void st_peer4(uint32_t a, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
-  return v;
 }
-__device__ __forceinline__ float2 ld_peer2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void st_peer2(uint32_t a, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // The weight of a partial result with maximum m in a sum with maximum top
@@ -135,10 +139,27 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   const int b = unit / p.N2, kvh = unit - b * p.N2;
 
   grid_dep_launch();
+  cluster_arrive();   // (waited for before the join's first remote store: every CTA runs by then)
   // Behind a prefix kernel (an ordinary launch, so everything before it is
   // complete) only the join has to wait for it.
   if (p.n_parts == 0) grid_dep_wait();
 
+  // ---------------------------------------------------------------- Q
+  // A fragments of the warp's 16 rows: lane (fg, ft) holds rows fg, fg + 8 at
+  // columns 2 ft, 2 ft + 1 and 8 + 2 ft, 9 + 2 ft of every 16.  Loaded ahead of
+  // the length, the page ids and the keys, which wait for one another.
+  const int r0 = rt * 16 + fg, r1 = r0 + 8;
+  const T* qp = static_cast<const T*>(p.q) + int64_t(b) * p.q_sb + 2 * ft;
+  const T* q0 = qp + int64_t(kvh * p.group + r0 / p.q_tokens) * p.q_sn + int64_t(r0 % p.q_tokens) * p.q_ss;
+  const T* q1 = qp + int64_t(kvh * p.group + r1 / p.q_tokens) * p.q_sn + int64_t(r1 % p.q_tokens) * p.q_ss;
+  uint32_t qa[KK][4];
+#pragma unroll
+  for (int kk = 0; kk < KK; ++kk) {
+    qa[kk][0] = r0 < p.rows ? *reinterpret_cast<const uint32_t*>(q0 + kk * 16) : 0u;
+    qa[kk][1] = r1 < p.rows ? *reinterpret_cast<const uint32_t*>(q1 + kk * 16) : 0u;
+    qa[kk][2] = r0 < p.rows ? *reinterpret_cast<const uint32_t*>(q0 + kk * 16 + 8) : 0u;
+    qa[kk][3] = r1 < p.rows ? *reinterpret_cast<const uint32_t*>(q1 + kk * 16 + 8) : 0u;
+  }
   const int L = p.kv_len == nullptr ? p.kv_max : min(max(p.kv_len[b], 0), p.kv_max);
   const int first = L - p.q_tokens;               // position of token 0 (may be negative: tokens that see nothing)
   // the tiles that hold a key some row may see: the sinks' [base / 16, t_sink)
@@ -203,23 +224,6 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   };
   for (int i = 0; i < ST - 1; ++i) issue(i);
 
-  // ---------------------------------------------------------------- Q
-  // A fragments of the warp's 16 rows: lane (fg, ft) holds rows fg, fg + 8 at
-  // columns 2 ft, 2 ft + 1 and 8 + 2 ft, 9 + 2 ft of every 16
-  const int r0 = rt * 16 + fg, r1 = r0 + 8;
-  const T* qp = static_cast<const T*>(p.q) + int64_t(b) * p.q_sb;
-  auto q_row = [&](int r) -> const T* {
-    return qp + int64_t(kvh * p.group + r / p.q_tokens) * p.q_sn + int64_t(r % p.q_tokens) * p.q_ss;
-  };
-  uint32_t qa[KK][4];
-#pragma unroll
-  for (int kk = 0; kk < KK; ++kk) {
-    const int c = kk * 16 + 2 * ft;
-    qa[kk][0] = r0 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r0) + c) : 0u;
-    qa[kk][1] = r1 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r1) + c) : 0u;
-    qa[kk][2] = r0 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r0) + c + 8) : 0u;
-    qa[kk][3] = r1 < p.rows ? *reinterpret_cast<const uint32_t*>(q_row(r1) + c + 8) : 0u;
-  }
   const int p0 = first + r0 % p.q_tokens, p1 = first + r1 % p.q_tokens;   // the rows' positions
   auto sees = [&](int pos, int j) -> bool {
     return j <= pos && j >= p.base && (j < p.sink || int64_t(pos) - j <= p.pre);
@@ -329,82 +333,83 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     ml[kg * 16 * MT + r1] = make_float2(m1, l1);
   }
   __syncthreads();
+  // This CTA's groups joined, float4 by float4, each sent to the CTA that
+  // writes it: CTA k of the cluster has items [k share, (k + 1) share).
   const int items = p.rows * (D / 4);
-  if (cs > 1) {
-    if (C::kGroups > 1) {
-      // this CTA's groups into group 0
-      float4 acc[(16 * MT * (D / 4) + kSpanThreads - 1) / kSpanThreads];
-      float2 mine = make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int w = 0; w < (16 * MT * (D / 4)) / kSpanThreads; ++w) {
-        const int e = w * kSpanThreads + threadIdx.x;
-        if (e >= items) break;
-        const int r = e / (D / 4), c4 = e % (D / 4);
-        float top = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) top = fmaxf(top, ml[g * 16 * MT + r].x);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
-          const float wt = join_weight(ml[g * 16 * MT + r].x, top);
-          const float4 x = *reinterpret_cast<const float4*>(ob + at(g, r, c4));
-          a.x += wt * x.x; a.y += wt * x.y; a.z += wt * x.z; a.w += wt * x.w;
-        }
-        acc[w] = a;
-      }
-      if (int(threadIdx.x) < p.rows) {
-        const int r = threadIdx.x;
-#pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) mine.x = fmaxf(mine.x, ml[g * 16 * MT + r].x);
-#pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
-          const float2 x = ml[g * 16 * MT + r];
-          mine.y += join_weight(x.x, mine.x) * x.y;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < (16 * MT * (D / 4)) / kSpanThreads; ++w) {
-        const int e = w * kSpanThreads + threadIdx.x;
-        if (e >= items) break;
-        *reinterpret_cast<float4*>(ob + at(0, e / (D / 4), e % (D / 4))) = acc[w];
-      }
-      if (int(threadIdx.x) < p.rows) ml[threadIdx.x] = mine;
-    }
-    cluster_sync_all();
-  }
-  if (p.n_parts > 0) grid_dep_wait();
-  const int n_own = cs > 1 ? int(cs) : C::kGroups;
-  const uint32_t ob_a = smem_u32(ob), ml_a = smem_u32(ml);
-  for (int e = int(rank) * kSpanThreads + threadIdx.x; e < items; e += int(cs) * kSpanThreads) {
+  const int share = (items + int(cs) - 1) / int(cs);
+  const uint32_t in_o = smem_u32(smem + C::kOffIn), in_ml = smem_u32(smem + C::kOffInML);
+  __syncwarp();
+  cluster_wait();
+  for (int e = threadIdx.x; e < items; e += kSpanThreads) {
     const int r = e / (D / 4), c4 = e % (D / 4);
-    const int head = kvh * p.group + r / p.q_tokens, tokn = r % p.q_tokens;
-    const int64_t prow = (int64_t(b) * p.N1 + head) * p.q_tokens + tokn;
-    auto own_ml = [&](int g) -> float2 {
-      return cs > 1 ? ld_peer2(peer_addr(ml_a + r * 8, g)) : ml[g * 16 * MT + r];
-    };
     float top = -INFINITY;
-    for (int g = 0; g < n_own; ++g) top = fmaxf(top, own_ml(g).x);
-#pragma unroll 4
-    for (int g = 0; g < p.n_parts; ++g) top = fmaxf(top, p.part_ml[g * p.part_rows + prow].x);
+#pragma unroll
+    for (int g = 0; g < C::kGroups; ++g) top = fmaxf(top, ml[g * 16 * MT + r].x);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-    for (int g = 0; g < n_own; ++g) {
-      const float2 x = own_ml(g);
-      const float w = join_weight(x.x, top);
-      const float4 y = cs > 1 ? ld_peer4(peer_addr(ob_a + at(0, r, c4) * 4, g))
-                              : *reinterpret_cast<const float4*>(ob + at(g, r, c4));
-      l += w * x.y;
-      a.x += w * y.x; a.y += w * y.y; a.z += w * y.z; a.w += w * y.w;
+#pragma unroll
+    for (int g = 0; g < C::kGroups; ++g) {
+      const float2 w2 = ml[g * 16 * MT + r];
+      const float w = join_weight(w2.x, top);
+      const float4 x = *reinterpret_cast<const float4*>(ob + at(g, r, c4));
+      l += w * w2.y;
+      a.x += w * x.x; a.y += w * x.y; a.z += w * x.z; a.w += w * x.w;
     }
-#pragma unroll 4
-    for (int g = 0; g < p.n_parts; ++g) {
-      const float2 x = p.part_ml[g * p.part_rows + prow];
-      const float w = join_weight(x.x, top);
-      float4 y = *reinterpret_cast<const float4*>(p.part_o + (g * p.part_rows + prow) * D + c4 * 4);
-      if (x.x == -INFINITY) y = make_float4(0.f, 0.f, 0.f, 0.f);   // an empty part's O may be 0 * NaN
-      l += w * x.y;
-      a.x += w * y.x; a.y += w * y.y; a.z += w * y.z; a.w += w * y.w;
+    const int owner = e / share;
+    st_peer4(peer_addr(in_o + (rank * share + e - owner * share) * 16, owner), a);
+    if (c4 == 0)
+      for (uint32_t k = 0; k < cs; ++k) st_peer2(peer_addr(in_ml + (rank * 16 * MT + r) * 8, k), make_float2(top, l));
+  }
+  __syncwarp();
+  cluster_arrive();
+  if (p.n_parts > 0) grid_dep_wait();   // (by every thread: the prefix's results are in)
+  cluster_wait();                       // nothing of this CTA is read or written by another from here on
+  const float4* xo = reinterpret_cast<const float4*>(smem + C::kOffIn);
+  const float2* xml = reinterpret_cast<const float2*>(smem + C::kOffInML);
+  for (int i = threadIdx.x; i < share; i += kSpanThreads) {
+    const int e = int(rank) * share + i;
+    if (e >= items) break;
+    const int r = e / (D / 4), c4 = e % (D / 4);
+    const int head = kvh * p.group + r / p.q_tokens, tokn = r % p.q_tokens;
+    float top = -INFINITY;
+    for (uint32_t g = 0; g < cs; ++g) top = fmaxf(top, xml[g * 16 * MT + r].x);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (uint32_t g = 0; g < cs; ++g) {
+      const float2 w2 = xml[g * 16 * MT + r];
+      const float w = join_weight(w2.x, top);
+      const float4 x = xo[g * share + i];
+      l += w * w2.y;
+      a.x += w * x.x; a.y += w * x.y; a.z += w * x.z; a.w += w * x.w;
+    }
+    // the prefix's parts, kBatch loads in flight, with a running maximum
+    constexpr int kBatch = 16;
+    const int64_t prow = (int64_t(b) * p.N1 + head) * p.q_tokens + tokn;
+    for (int g0 = 0; g0 < p.n_parts; g0 += kBatch) {
+      float2 w2[kBatch];
+      float4 x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const bool in = g0 + k < p.n_parts;
+        const int64_t row = (in ? g0 + k : g0) * p.part_rows + prow;
+        w2[k] = p.part_ml[row];
+        x[k] = *reinterpret_cast<const float4*>(p.part_o + row * D + c4 * 4);
+        if (!in) w2[k].x = -INFINITY;
+      }
+      float t = top;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) t = fmaxf(t, w2[k].x);
+      const float keep = join_weight(top, t);
+      l *= keep;
+      a.x *= keep; a.y *= keep; a.z *= keep; a.w *= keep;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (w2[k].x == -INFINITY) continue;   // an empty part: its O may be 0 * NaN
+        const float w = join_weight(w2[k].x, t);
+        l += w * w2[k].y;
+        a.x += w * x[k].x; a.y += w * x[k].y; a.z += w * x[k].z; a.w += w * x[k].w;
+      }
+      top = t;
     }
     const bool has = l != 0.f;   // a NaN sum stays a NaN
     const float inv = has ? 1.f / l : 0.f;
@@ -417,7 +422,6 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
       p.lse[int64_t(b) * p.lse_sb + int64_t(head) * p.lse_sn + int64_t(tokn) * p.lse_ss] =
           has ? (top + __log2f(l)) * 0.69314718055994531f : INFINITY;
   }
-  if (cs > 1) cluster_sync_all();   // no CTA leaves while another reads its shared memory
 }
 
 template <int D, bool BF16, int MT>
@@ -451,7 +455,7 @@ cudaError_t launch_span_decode(const SpanParams& p, int head_dim, bool bf16, int
   const int64_t tiles = span / kSpanTile + 1;
   const int64_t units = int64_t(p.B) * p.N2;
   int cs = 1;
-  while (cs < 8 && units * cs < 2 * n_sm && tiles >= int64_t(4) * cs * (4 / mt)) cs *= 2;
+  while (cs < kMostCtas && units * cs < 2 * n_sm && tiles >= int64_t(4) * cs * (4 / mt)) cs *= 2;
 #define FIA_SPAN(DD, BB)                                    \
   switch (mt) {                                             \
     case 1: return launch_one<DD, BB, 1>(p, cs, s);         \
