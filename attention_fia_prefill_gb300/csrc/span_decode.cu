@@ -13,11 +13,13 @@
 //   * Work: a cluster of 1..8 CTAs runs a unit, each CTA four warps.  A warp
 //     owns 16 rows (mma.sync m16n8k16); units of up to 16 rows give each warp
 //     keys of its own (tile v of the list belongs to group v mod groups), those
-//     of 32 / 64 rows pair / quadruple the warps of a group over the same tiles.
+//     of 32 / 64 rows pair / quadruple the warps of a group over the same tiles,
+//     two / four of them a step.
 //   * Data: a group streams its tiles through a ring of its own with cp.async
 //     (16-byte pieces, XOR-swizzled so that ldmatrix has no bank conflicts): no
 //     barrier across groups in the loop.  A tile lies in one page (16 divides
-//     the page size); page ids come 32 at a time, one per lane, a batch ahead.
+//     the page size); page ids come 32 at a time, one per lane, a batch ahead,
+//     and become cache offsets there (one division per tile, not per piece).
 //     Keys that no row sees are not read: they are zero-filled (a freed page
 //     behind the window may hold anything, and 0 * NaN would reach the sums).
 //   * Softmax: running maximum and sum per row and group in fp32, scores in
@@ -44,10 +46,14 @@ constexpr int kMostCtas = 8;         // CTAs of a unit (a portable cluster)
 template <int D, int MT>
 struct SpanCfg {
   static constexpr int kGroups = 4 / MT;
-  // per group; about the same bytes in flight for every MT, two CTAs per SM
-  static constexpr int kStages = MT == 1 ? 3 : MT == 2 ? 5 : 8;
+  // CTAs per SM (registers and shared memory allow it)
+  static constexpr int kResident = D == 64 ? 4 : 2;
+  // A step takes kSub tiles: the warps of a wider group wait for one another
+  // once a step, and their products and row maxima need the work to hide in.
+  static constexpr int kSub = MT;
+  static constexpr int kStages = MT == 1 ? 3 : 2;   // steps in a group's ring
   static constexpr int kTileBytes = kSpanTile * D * 2;    // K or V
-  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStageBytes = 2 * kSub * kTileBytes;
   static constexpr int kRing = kGroups * kStages * kStageBytes;
   // after the loop the rings hold O of every group [kGroups][16 MT][D]
   static constexpr int kO = kGroups * 16 * MT * D * 4;
@@ -122,13 +128,13 @@ __device__ __forceinline__ void st_peer2(uint32_t a, float2 v) {
 __device__ __forceinline__ float join_weight(float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); }
 
 template <int D, bool BF16, int MT>
-__global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __grid_constant__ SpanParams p) {
+__global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_decode_kernel(const __grid_constant__ SpanParams p) {
   using C = SpanCfg<D, MT>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int CH = D / 8;                       // 16-byte pieces of a row
   constexpr int KK = D / 16;                      // k-steps of Q K^T
   constexpr int NT = D / 8;                       // n-tiles of O
-  constexpr int ST = C::kStages;
+  constexpr int ST = C::kStages, SUB = C::kSub;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -167,51 +173,73 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   const int t_end = (L + kSpanTile - 1) / kSpanTile;
   const int t_base = p.base / kSpanTile;
   const int t_sink = min(t_end, max(t_base, (p.sink + kSpanTile - 1) / kSpanTile));
-  const int64_t win = int64_t(first) - p.pre;     // first key of token 0's window
-  const int t_win = max(t_sink, int(max(win, int64_t(0)) / kSpanTile));
+  const int win = int(max(int64_t(first) - p.pre, int64_t(0)));   // first key of token 0's window
+  const int t_win = max(t_sink, win / kSpanTile);
   const int n_sink = max(0, t_sink - t_base);
   const int n_tiles = n_sink + max(0, t_end - t_win);
   const int groups = int(cs) * C::kGroups;
   const int gi = int(rank) * C::kGroups + kg;
-  const int n = n_tiles > gi ? (n_tiles - gi + groups - 1) / groups : 0;
-  auto tile_key = [&](int i) -> int {             // first key of the group's i-th tile
-    const int v = gi + i * groups;
+  const int n_steps = (n_tiles + SUB - 1) / SUB;
+  const int n = n_steps > gi ? (n_steps - gi + groups - 1) / groups : 0;   // this group's steps
+  // First key of tile u of the group's i-th step; past the list it is L or more.
+  // Without a window the list has no gap, and page ids load beside the length.
+  const bool gapless = p.pre >= p.kv_max;
+  auto tile_key = [&](int i, int u) -> int {
+    const int v = (gi + i * groups) * SUB + u;
+    if (gapless) return (t_base + v) * kSpanTile;
     return (v < n_sink ? t_base + v : t_win + v - n_sink) * kSpanTile;
   };
 
   // ---------------------------------------------------------------- loads
-  auto page_of = [&](int i) -> int {              // block id of the group's i-th tile; -1: none
-    if (i >= n) return -1;
-    if (p.block_table == nullptr) return b;
-    const int id = p.block_table[int64_t(b) * p.table_stride + tile_key(i) / p.block_size];
-    return id >= 0 && id < p.n_blocks ? id : -1;
+  // where the group's q-th tile (step q / SUB) starts in the caches, in
+  // elements; -1: nowhere.  32 tiles at a time, one per lane, a batch ahead.
+  auto start_of = [&](int q) -> int64_t {
+    const int j = tile_key(q / SUB, q % SUB);
+    if (p.block_table == nullptr) return int64_t(b) * p.blk_stride + int64_t(j) * p.row_stride;
+    const int page = j / p.block_size;
+    if (page >= p.table_stride) return -1;
+    const int id = p.block_table[int64_t(b) * p.table_stride + page];
+    if (id < 0 || id >= p.n_blocks) return -1;
+    return int64_t(id) * p.blk_stride + int64_t(j - page * p.block_size) * p.row_stride;
   };
-  int ids = page_of(lane), ids_next = page_of(32 + lane), ids_blk = 0;
+  int64_t starts = start_of(lane), starts_next = -1;
+  int batch = 0;
   const uint32_t ring = smem_u32(smem) + kg * ST * C::kStageBytes;
-  const T* kp = static_cast<const T*>(p.k) + kvh * p.head_stride;
-  const T* vp = static_cast<const T*>(p.v) + kvh * p.head_stride;
+  // this lane's first piece of a tile, and the rows between its pieces
+  constexpr int kIts = kSpanTile * CH / (32 * MT), kRowStep = 32 * MT / CH;
+  const int row_l = (rt * 32 + lane) / CH, c_l = (rt * 32 + lane) % CH;
+  const int64_t lane_off = int64_t(kvh) * p.head_stride + int64_t(row_l) * p.row_stride + c_l * 8;
+  const T* kp = static_cast<const T*>(p.k) + lane_off;
+  const T* vp = static_cast<const T*>(p.v) + lane_off;
+  const int64_t it_off = int64_t(kRowStep) * p.row_stride;
   auto issue = [&](int i) {
-    if ((i >> 5) != ids_blk) {
-      ids = ids_next;
-      ++ids_blk;
-      ids_next = page_of(((ids_blk + 1) << 5) + lane);
+    if ((i * SUB >> 5) != batch) {
+      starts = starts_next;
+      ++batch;
     }
-    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-    if (i < n) {
-      const int j0 = tile_key(i);
-      const int in_page = p.block_table == nullptr ? j0 : j0 % p.block_size;
-      const uint32_t st = ring + (i % ST) * C::kStageBytes;
-      const int64_t off0 = int64_t(max(id, 0)) * p.blk_stride + int64_t(in_page) * p.row_stride;
+    if ((i * SUB & 31) == 0 && i + 32 / SUB < n) starts_next = start_of(((batch + 1) << 5) + lane);
 #pragma unroll
-      for (int it = 0; it < kSpanTile * CH / (32 * MT); ++it) {
-        const int idx = it * 32 * MT + rt * 32 + lane;
-        const int row = idx / CH, c = idx % CH;
-        const int j = j0 + row;
-        const bool live = id >= 0 && j < L && j >= p.base && (j < p.sink || j >= win);
-        const uint32_t dst = st + row * (D * 2) + ((c ^ (row & 7)) << 4);
-        const int64_t off = live ? off0 + int64_t(row) * p.row_stride + c * 8 : 0;
-        cp_async_zfill<16>(dst, kp + off, live ? 16u : 0u);
-        cp_async_zfill<16>(dst + C::kTileBytes, vp + off, live ? 16u : 0u);
+    for (int u = 0; u < SUB; ++u) {
+      const int64_t at = __shfl_sync(0xffffffffu, starts, (i * SUB + u) & 31);
+      if (i < n) {
+        const int j0 = tile_key(i, u);
+        const uint32_t st = ring + (i % ST) * C::kStageBytes + u * C::kTileBytes + row_l * (D * 2);
+        // every key of the tile is one that some row sees
+        const bool whole = at >= 0 && j0 + kSpanTile <= L && j0 >= p.base && (j0 + kSpanTile <= p.sink || j0 >= win);
+        const T* ks = kp + (at >= 0 ? at : 0);
+        const T* vs = vp + (at >= 0 ? at : 0);
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+          const uint32_t dst = st + it * kRowStep * (D * 2) + ((c_l ^ ((row_l + it * kRowStep) & 7)) << 4);
+          uint32_t bytes = 16u;
+          if (!whole) {
+            const int j = j0 + row_l + it * kRowStep;
+            bytes = at >= 0 && j < L && j >= p.base && (j < p.sink || j >= win) ? 16u : 0u;
+          }
+          // (a piece of 0 bytes reads nothing; its address still names the cache)
+          cp_async_zfill<16>(dst, bytes != 0u ? ks + it * it_off : static_cast<const T*>(p.k), bytes);
+          cp_async_zfill<16>(dst + SUB * C::kTileBytes, bytes != 0u ? vs + it * it_off : static_cast<const T*>(p.v), bytes);
+        }
       }
     }
     cp_async_commit();
@@ -225,9 +253,9 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   for (int i = 0; i < ST - 1; ++i) issue(i);
 
   const int p0 = first + r0 % p.q_tokens, p1 = first + r1 % p.q_tokens;   // the rows' positions
-  auto sees = [&](int pos, int j) -> bool {
-    return j <= pos && j >= p.base && (j < p.sink || int64_t(pos) - j <= p.pre);
-  };
+  const int w0 = int(max(int64_t(p0) - p.pre, int64_t(0))), w1 = int(max(int64_t(p1) - p.pre, int64_t(0)));
+  const int win_last = int(max(int64_t(L) - 1 - p.pre, int64_t(0)));   // the last token's window
+  auto sees = [&](int pos, int w, int j) -> bool { return j <= pos && j >= p.base && (j < p.sink || j >= w); };
 
   // ---------------------------------------------------------------- the loop
   float o[NT][4];
@@ -242,33 +270,46 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     cp_async_wait_group<ST - 2>();
     group_sync();            // the tile is in for every warp of the group, and the slot before it has been read
     issue(i + ST - 1);
-    const uint32_t ks = ring + (i % ST) * C::kStageBytes, vs = ks + C::kTileBytes;
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const uint32_t ks = ring + (i % ST) * C::kStageBytes, vs = ks + SUB * C::kTileBytes;
+    float s[2 * SUB][4];
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      // matrices: keys 0-7 | 0-7 | 8-15 | 8-15, pieces 2 kk | 2 kk + 1 | ...
-      uint32_t f[4];
-      const int row = (lm >> 1) * 8 + lr, c = 2 * kk + (lm & 1);
-      ldsm4(ks + row * (D * 2) + ((c ^ lr) << 4), f);
-      mma16<BF16>(s[0], qa[kk], f[0], f[1]);
-      mma16<BF16>(s[1], qa[kk], f[2], f[3]);
+    for (int h = 0; h < 2 * SUB; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[h][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        // matrices: keys 0-7 | 0-7 | 8-15 | 8-15, pieces 2 kk | 2 kk + 1 | ...
+        uint32_t f[4];
+        const int row = (lm >> 1) * 8 + lr, c = 2 * kk + (lm & 1);
+        ldsm4(ks + u * C::kTileBytes + row * (D * 2) + ((c ^ lr) << 4), f);
+        mma16<BF16>(s[2 * u], qa[kk], f[0], f[1]);
+        mma16<BF16>(s[2 * u + 1], qa[kk], f[2], f[3]);
+      }
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const int j0 = tile_key(i, u);
+      // every row sees every key of the tile
+      const bool full = j0 + kSpanTile - 1 <= first && j0 >= p.base &&
+                        (j0 + kSpanTile <= p.sink || j0 >= win_last);
+      if (!full) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = j0 + 8 * h + 2 * ft + e;
+            if (!sees(p0, w0, j)) s[2 * u + h][e] = -INFINITY;
+            if (!sees(p1, w1, j)) s[2 * u + h][2 + e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int h = 2 * u; h < 2 * u + 2; ++h) {
+        x0 = fmax3(x0, s[h][0], s[h][1]);
+        x1 = fmax3(x1, s[h][2], s[h][3]);
+      }
     }
-    const int j0 = tile_key(i);
-    // every row sees every key of the tile
-    const bool full = j0 + kSpanTile - 1 <= first && j0 >= p.base &&
-                      (j0 + kSpanTile <= p.sink || j0 >= win + p.q_tokens - 1);
-    if (!full) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = j0 + 8 * h + 2 * ft + e;
-          if (!sees(p0, j)) s[h][e] = -INFINITY;
-          if (!sees(p1, j)) s[h][2 + e] = -INFINITY;
-        }
-    }
-    float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-    float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
@@ -289,24 +330,28 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
       m1 = n1;
     }
     const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-    uint32_t pa[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float y0 = fast_exp2(fmaf(s[h][0], sl2, -z0)), y1 = fast_exp2(fmaf(s[h][1], sl2, -z0));
-      const float y2 = fast_exp2(fmaf(s[h][2], sl2, -z1)), y3 = fast_exp2(fmaf(s[h][3], sl2, -z1));
-      l0 += y0 + y1;
-      l1 += y2 + y3;
-      pa[2 * h] = pack2(y0, y1, BF16);
-      pa[2 * h + 1] = pack2(y2, y3, BF16);
-    }
+    for (int u = 0; u < SUB; ++u) {
+      uint32_t pa[4];
 #pragma unroll
-    for (int t = 0; t < NT; t += 2) {
-      // matrices: keys 0-7 | 8-15 of piece t, then of piece t + 1
-      uint32_t f[4];
-      const int row = (lm & 1) * 8 + lr, c = t + (lm >> 1);
-      ldsm4_trans(vs + row * (D * 2) + ((c ^ lr) << 4), f);
-      mma16<BF16>(o[t], pa, f[0], f[1]);
-      mma16<BF16>(o[t + 1], pa, f[2], f[3]);
+      for (int h = 0; h < 2; ++h) {
+        const float* x = s[2 * u + h];
+        const float y0 = fast_exp2(fmaf(x[0], sl2, -z0)), y1 = fast_exp2(fmaf(x[1], sl2, -z0));
+        const float y2 = fast_exp2(fmaf(x[2], sl2, -z1)), y3 = fast_exp2(fmaf(x[3], sl2, -z1));
+        l0 += y0 + y1;
+        l1 += y2 + y3;
+        pa[2 * h] = pack2(y0, y1, BF16);
+        pa[2 * h + 1] = pack2(y2, y3, BF16);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        // matrices: keys 0-7 | 8-15 of piece t, then of piece t + 1
+        uint32_t f[4];
+        const int row = (lm & 1) * 8 + lr, c = t + (lm >> 1);
+        ldsm4_trans(vs + u * C::kTileBytes + row * (D * 2) + ((c ^ lr) << 4), f);
+        mma16<BF16>(o[t], pa, f[0], f[1]);
+        mma16<BF16>(o[t + 1], pa, f[2], f[3]);
+      }
     }
   }
   cp_async_wait_all();
@@ -383,7 +428,7 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
       a.x += w * x.x; a.y += w * x.y; a.z += w * x.z; a.w += w * x.w;
     }
     // the prefix's parts, kBatch loads in flight, with a running maximum
-    constexpr int kBatch = 16;
+    constexpr int kBatch = D == 64 ? 16 : 24;
     const int64_t prow = (int64_t(b) * p.N1 + head) * p.q_tokens + tokn;
     for (int g0 = 0; g0 < p.n_parts; g0 += kBatch) {
       float2 w2[kBatch];
@@ -445,17 +490,33 @@ cudaError_t launch_one(const SpanParams& p, int cs, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, span_decode_kernel<D, BF16, MT>, p);
 }
 
+// CTAs of a unit: those whose waves take the least time, a CTA costing its
+// groups' tiles and about kSpanStart more (launch, length, page ids, first
+// keys, join).  Where the keys' limit is not the window's but the tables'
+// the lengths behind it vary, and smaller shares even them out: up to a
+// seventh more by this count is taken for them.  (Sweep over 1, 2, 4, 8 CTAs,
+// us: 16 sequences x 8 heads, window of 65 tiles 24.0, 17.8, 25.6, 41.1; 64 x 8,
+// 257 tiles 170, 193, 197, 273; 32 x 8, lengths up to 513 tiles 133, 113, 106, 128.)
+constexpr int kSpanStart = 4;
+int cluster_ctas(int64_t units, int64_t tiles, int groups, bool even, int64_t slots) {
+  int best = 1;
+  int64_t least = 0;
+  for (int cs = 1; cs <= kMostCtas; cs *= 2) {
+    const int64_t waves = (units * cs + slots - 1) / slots;
+    const int64_t cost = waves * ((tiles + cs * groups - 1) / (cs * groups) + kSpanStart);
+    if (cs == 1 || (even ? cost < least : cost * 7 < least * 8)) best = cs;
+    if (cs == 1 || cost < least) least = cost;
+  }
+  return best;
+}
+
 }  // namespace
 
 cudaError_t launch_span_decode(const SpanParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s) {
   const int mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
-  // CTAs of a unit: enough to fill the GPU (two CTAs per SM), as long as a
-  // group keeps two tiles
   const int64_t span = std::min<int64_t>(p.kv_max - p.base, int64_t(p.sink) + p.pre + p.q_tokens);
-  const int64_t tiles = span / kSpanTile + 1;
-  const int64_t units = int64_t(p.B) * p.N2;
-  int cs = 1;
-  while (cs < kMostCtas && units * cs < 2 * n_sm && tiles >= int64_t(4) * cs * (4 / mt)) cs *= 2;
+  const int cs = cluster_ctas(int64_t(p.B) * p.N2, span / kSpanTile + 1, 4 / mt,
+                              span < p.kv_max - p.base, (head_dim == 64 ? 4 : 2) * n_sm);
 #define FIA_SPAN(DD, BB)                                    \
   switch (mt) {                                             \
     case 1: return launch_one<DD, BB, 1>(p, cs, s);         \
