@@ -8,9 +8,10 @@ namespace fia {
 namespace {
 
 constexpr int kTableThreads = 256;
-constexpr int kTablePer = 4;                                   // requests a thread scans
-constexpr int kTableChunk = kTableThreads * kTablePer;         // requests scanned at once
-constexpr int kTableTokens = 1024;                             // tokens a CTA writes
+constexpr int kTablePer = 4;                                   // requests a thread scans, tokens it writes
+constexpr int kTableChunk = kTableThreads * kTablePer;         // requests scanned at once; tokens of a CTA
+
+__device__ __forceinline__ uint32_t ceil_div(uint32_t a, uint32_t b) { return a / b + (a % b != 0u); }
 
 // Sum over the block of everything before this thread (and the total), two
 // 64-bit values at once: lengths are 32-bit, their sums need not be.
@@ -49,33 +50,41 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t& ta,
 // and needs ceil((context + new) / bs); the blocks it lacks are the free
 // list's entries from E_b, the blocks asked for by the requests before it.
 // Every CTA scans the requests (new tokens and blocks, kTableChunk at a time)
-// and writes the slots of its kTableTokens tokens, which it finds by a binary
-// search in the running sum of new tokens.  A new block's first position is a
-// new token (have * bs >= context), and the thread that has this token writes
-// the block's table entry: no second pass, and no entry is both read and
-// written (slots in older blocks come from entries below have).
-// Bound: a launch and two dependent loads; the scan of 512 requests repeated
-// by every CTA costs less than a launch of its own.
+// and writes the slots of its kTableChunk tokens, four consecutive ones to a
+// thread, which finds the first by a binary search in the running sum of new
+// tokens and steps on from there.  A new block's first position is a new token
+// (have * bs >= context), and the thread that has this token writes the
+// block's table entry: no second pass, and no entry is both read and written
+// (slots in older blocks come from entries below have).
+// Bound: a launch and three dependent loads (lengths, block, slot); the scan
+// repeated by every CTA costs less than a launch of its own.
 __global__ void __launch_bounds__(kTableThreads) block_table_kernel(const TableParams p) {
   __shared__ int64_t sh[kTableThreads / 32][2];
   __shared__ int s_cu[kTableChunk];        // new tokens up to and with the request, within the chunk
   __shared__ int s_ctx[kTableChunk];
   __shared__ int64_t s_blk[kTableChunk];   // blocks asked for before the request
-  const int bs = p.block_size;
-  const int64_t t0 = int64_t(blockIdx.x) * kTableTokens;
-  const int64_t t1 = min(t0 + kTableTokens, int64_t(p.n_tokens));
+  const uint32_t bs = uint32_t(p.block_size);
+  const int64_t t0 = int64_t(blockIdx.x) * kTableChunk;
+  const int64_t t1 = min(t0 + kTableChunk, int64_t(p.n_tokens));
+  const int64_t mine = t0 + int64_t(threadIdx.x) * kTablePer;   // this thread's first token
   const bool lead = blockIdx.x == 0;
-  int64_t tok = 0, blk = 0;   // before this chunk
+  int slot[kTablePer];
+#pragma unroll
+  for (int k = 0; k < kTablePer; ++k) slot[k] = -1;
+  int64_t tok = 0, blk = 0;   // before this chunk of requests
   for (int base = 0; base < p.B && (lead || tok < t1); base += kTableChunk) {
-    int ctx[kTablePer], add[kTablePer], nb[kTablePer];
+    int ctx[kTablePer], add[kTablePer];
+    uint32_t nb[kTablePer];
     int64_t st = 0, sb = 0;
 #pragma unroll
     for (int i = 0; i < kTablePer; ++i) {
       const int b = base + int(threadIdx.x) * kTablePer + i;
       ctx[i] = b < p.B ? max(p.context_lens[b], 0) : 0;
       add[i] = b < p.B ? max(p.new_lens[b], 0) : 0;
-      const int64_t total = int64_t(ctx[i]) + add[i];
-      nb[i] = int((total + bs - 1) / bs - (int64_t(ctx[i]) + bs - 1) / bs);
+    }
+#pragma unroll
+    for (int i = 0; i < kTablePer; ++i) {
+      nb[i] = ceil_div(uint32_t(ctx[i]) + uint32_t(add[i]), bs) - ceil_div(uint32_t(ctx[i]), bs);
       st += add[i];
       sb += nb[i];
     }
@@ -96,38 +105,50 @@ __global__ void __launch_bounds__(kTableThreads) block_table_kernel(const TableP
       }
     }
     __syncthreads();
-    const int64_t lo = max(t0, tok), hi = min(t1, tok + ct);
-    const int n = min(kTableChunk, p.B - base);
-    for (int64_t t = lo + threadIdx.x; t < hi; t += kTableThreads) {
-      const int x = int(t - tok);
-      int l = 0, r = n - 1;   // the first request whose running sum is above x
+    // this thread's tokens of this chunk's requests: [lo, hi)
+    const int64_t lo = max(mine, tok), hi = min(min(mine + kTablePer, t1), tok + ct);
+    if (lo < hi) {
+      int l = 0, r = min(kTableChunk, p.B - base) - 1;   // the first request whose running sum is above lo
+      const int x0 = int(lo - tok);
       while (l < r) {
         const int m = (l + r) >> 1;
-        if (s_cu[m] > x) r = m; else l = m + 1;
+        if (s_cu[m] > x0) r = m; else l = m + 1;
       }
-      const int64_t pos = int64_t(s_ctx[l]) + x - (l > 0 ? s_cu[l - 1] : 0);
-      const int64_t page = pos / bs;
-      const int off = int(pos - page * bs);
-      const int64_t have = (int64_t(s_ctx[l]) + bs - 1) / bs;
-      int32_t* row = p.block_table + int64_t(base + l) * p.table_cols;
-      int id = -1;
-      if (page < p.table_cols) {
-        if (page < have) {
-          id = row[page];
-        } else {
-          const int64_t f = s_blk[l] + page - have;
-          if (f < p.n_free) id = p.free_blocks[f];
-          if (off == 0) row[page] = id;
+#pragma unroll
+      for (int k = 0; k < kTablePer; ++k) {
+        const int64_t t = mine + k;
+        if (t < lo || t >= hi) continue;
+        const int x = int(t - tok);
+        while (s_cu[l] <= x) ++l;
+        const uint32_t pos = uint32_t(s_ctx[l]) + uint32_t(x - (l > 0 ? s_cu[l - 1] : 0));
+        const uint32_t page = pos / bs, off = pos - page * bs, have = ceil_div(uint32_t(s_ctx[l]), bs);
+        int32_t* row = p.block_table + int64_t(base + l) * p.table_cols;
+        int id = -1;
+        if (page < uint32_t(p.table_cols)) {
+          if (page < have) {
+            id = row[page];
+          } else {
+            const int64_t f = s_blk[l] + (page - have);
+            if (f < p.n_free) id = p.free_blocks[f];
+            if (off == 0) row[page] = id;
+          }
         }
+        const int64_t at = int64_t(id) * bs + off;
+        slot[k] = id < 0 || at > 0x7fffffff ? -1 : int(at);
       }
-      const int64_t slot = int64_t(id) * bs + off;
-      p.slot_mapping[t] = id < 0 || slot > 0x7fffffff ? -1 : int(slot);
     }
     tok += ct;
     blk += cb;
     __syncthreads();
   }
-  for (int64_t t = max(t0, tok) + threadIdx.x; t < t1; t += kTableThreads) p.slot_mapping[t] = -1;
+  int32_t* out = p.slot_mapping + mine;
+  if (mine + kTablePer <= t1 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+    *reinterpret_cast<int4*>(out) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kTablePer; ++k)
+      if (mine + k < t1) out[k] = slot[k];
+  }
   if (lead && threadIdx.x == 0) p.num_blocks[0] = int(min(blk, int64_t(0x7fffffff)));
 }
 
@@ -163,7 +184,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheWriteParams
 }  // namespace
 
 cudaError_t launch_block_table(const TableParams& p, cudaStream_t s) {
-  const unsigned grid = unsigned(std::max<int64_t>(1, (int64_t(p.n_tokens) + kTableTokens - 1) / kTableTokens));
+  const unsigned grid = unsigned(std::max<int64_t>(1, (int64_t(p.n_tokens) + kTableChunk - 1) / kTableChunk));
   block_table_kernel<<<grid, kTableThreads, 0, s>>>(p);
   return cudaGetLastError();
 }

@@ -293,6 +293,19 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
     na = int(int64_t(tiles) * (it.cost + 1) / p.n_splits) - jt0;
     nb = has_b ? na : 0;
   }
+  // window with sinks: the columns a product takes of its tile, a multiple of
+  // 16: those of the sinks in the last tile before the band, and in tile B's
+  // first band tile when its window starts past it; else all 128
+  int cols_sink = kTileN, cols_b = kTileN;
+  if (MODE == kWindow) {
+    auto sinks_of = [&](int tile) -> int { return min((max(p.sink - tile * kTileN, 1) + 15) & ~15, kTileN); };
+    cols_sink = sinks_of(max(n_sink - 1, 0));
+    if (int64_t(jt0 + 1) * kTileN <= q0 + kTileM + win_d - p.band_pre) cols_b = sinks_of(jt0);
+  }
+  auto columns = [&](int t, int j) -> int {
+    if (MODE != kWindow) return kTileN;
+    return j == n_sink - 1 ? cols_sink : (t == 1 && j == n_sink) ? cols_b : kTileN;
+  };
   // K/V tile of the walk's step j
   auto tile_of = [&](int j) -> int { return MODE == kWindow ? (j < n_sink ? j : jt0 + j - n_sink) : jt0 + j; };
   const int nl = max(na, nb);
@@ -442,6 +455,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, BF16 ? 1 : 0, 0, 0);
+      constexpr uint32_t idesc_qk0 = idesc_f16(128, 0, BF16 ? 1 : 0, 0, 0);   // without its N
       constexpr uint32_t idesc_pv = idesc_f16(128, DV, BF16 ? 1 : 0, 0, 1);
       // Descriptors of every operand buffer, built once; an MMA's K-slice
       // only moves the start address (bits 0..13, in 16-byte units), which
@@ -465,10 +479,11 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         const uint64_t qd = t == 0 ? qd0 : qd1;
         const uint64_t kd = kd0 + uint64_t(s) * kStepK;
         const uint32_t dst = tmem + t * 128;
+        const uint32_t idesc = MODE == kWindow ? idesc_qk0 | (uint32_t(columns(t, j)) >> 3 << 17) : idesc_qk;
 #pragma unroll
         for (int kk = 0; kk < DQK / 16; ++kk) {
           const uint64_t off = uint64_t(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
-          mma_ss(dst, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+          mma_ss(dst, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
         }
         mma_commit(&s_full[3 * t + s]);
         last_bar = &s_full[3 * t + s];
@@ -486,9 +501,15 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         const uint64_t vd = vd0 + uint64_t(s) * kStepV;
         const uint32_t dst = tmem + C::kColO + t * DV;
         const uint32_t pt = tmem + t * 128;
+        const int cols = columns(t, j);
+        if (MODE != kWindow || cols == kTileN) {
 #pragma unroll
-        for (int kk = 0; kk < kTileN / 16; ++kk)
-          mma_ts(dst, pt + kk * 8, vd + uint64_t((kk * 2048) >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kTileN / 16; ++kk)
+            mma_ts(dst, pt + kk * 8, vd + uint64_t((kk * 2048) >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+        } else {
+          for (int kk = 0; kk < cols / 16; ++kk)
+            mma_ts(dst, pt + kk * 8, vd + uint64_t((kk * 2048) >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+        }
         if (t == 0 && nb > 0) {
           if (j == na - 1) {
             mma_commit(pva_done);
@@ -593,7 +614,20 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       ph = r % p.group;
       if (pb < p.n_batch) p_end = min(max(max(p.kv_lens[pb], 0) - p.q_tokens + pt + 1, 0), p.s2);
     }
+    // kWindow: the row's position (lengths and pre are at most 2^30)
+    const int w_pos = MODE == kWindow ? i + int(win_d) : 0;
     const bool warp_rows = MODE != kPrefix || __any_sync(0xffffffffu, pb < p.n_batch);
+    auto rescale_o = [&](float alpha) {
+#pragma unroll 1
+      for (int c = 0; c < DV / 16; ++c) {
+        uint32_t u[16];
+        tmem_ld16(tmem + lane_off + col_o + c * 16, u);
+        tmem_wait_ld(u);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+        tmem_st16(tmem + lane_off + col_o + c * 16, u);
+      }
+    };
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -649,16 +683,71 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         continue;
       }
       if constexpr (MODE == kWindow) {
-        // the warp's rows see keys up to row 31's position and from row 0's
-        // window or the sinks: a tile outside both has P = 0 (as above)
         const int kw = tile_of(j) * kTileN;
-        const int64_t p_lo = int64_t(i - lane) + win_d;
-        if (kw > p_lo + 31 || (kw >= p.sink && kw + kTileN - 1 < p_lo - p.band_pre)) {
-          uint32_t z[16];
+        // the first and the last row's last key and window
+        const int pos_0 = w_pos - lane, pos_31 = pos_0 + 31;
+        const int lim_0 = min(bi.kv_len - 1, pos_0), lim_31 = min(bi.kv_len - 1, pos_31);
+        const int lo_0 = pos_0 - p.band_pre, lo_31 = pos_31 - p.band_pre;
+        if (kw + kTileN - 1 > lim_0 || kw < lo_31) {
+          // A tile on an edge of the warp's rows, 32 columns at a time: those
+          // that no row sees are neither loaded nor exponentiated (P = 0).  Two
+          // passes over S, so that this path needs few registers: masks in the
+          // full tiles' path below cost it a quarter of its speed.
+          auto hid = [&](int k0) -> bool { return k0 > lim_31 || (k0 >= p.sink && k0 + 31 < lo_0); };
+          // columns [0, sinks) and [from, to] of the piece are the row's
+          auto piece = [&](int q, uint32_t (&su)[32]) {
+            tmem_ld32(tmem + lane_off + col_s + 32 * q, su);
+            const int k0 = kw + 32 * q, to = min(bi.kv_len - 1, w_pos) - k0, from = w_pos - p.band_pre - k0;
+            const int sinks = min(p.sink - k0, to + 1);
+            tmem_wait_ld(su);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) z[e] = 0u;
+            for (int e = 0; e < 32; ++e)
+              if (e > to || (e < from && e >= sinks)) su[e] = __float_as_uint(-INFINITY);
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            if (hid(kw + 32 * q)) continue;
+            uint32_t su[32];
+            piece(q, su);
+            float a[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_off + col_s + c * 16, z);
+            for (int k = 0; k < 4; ++k) a[k] = fmaxf(__uint_as_float(su[k]), __uint_as_float(su[4 + k]));
+#pragma unroll
+            for (int c = 8; c < 32; c += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) a[k] = fmax3(a[k], __uint_as_float(su[c + k]), __uint_as_float(su[c + 4 + k]));
+            top = fmax3(top, fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+          }
+          const float m_new = fmaxf(m, top * sl2);
+          const float m_use = (m == -INFINITY || m_new > m + 8.f) ? m_new : m;   // as below
+          const float alpha = (m_use == m) ? 1.f : fast_exp2(m - m_use);
+          const float mo = (m_use == -INFINITY) ? 0.f : m_use;
+          uint64_t acc2[2] = {0ull, 0ull};   // summed in the full tiles' order
+          // (P of a piece takes columns of pieces that have been read)
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t u[16];
+            if (hid(kw + 32 * q)) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = 0u;
+            } else {
+              uint32_t su[32];
+              piece(q, su);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float y0 = fast_exp2(fmaf(__uint_as_float(su[2 * e]), sl2, -mo));
+                const float y1 = fast_exp2(fmaf(__uint_as_float(su[2 * e + 1]), sl2, -mo));
+                acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(y0, y1));
+                u[e] = pack2(y0, y1, BF16);
+              }
+            }
+            tmem_st16(tmem + lane_off + col_s + q * 16, u);
+          }
+          float s0, s1;
+          f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
+          l = l * alpha + (s0 + s1);
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
           if (kw + kTileN > bi.kv_len && (t == 0 || j >= na) && !clear_v_tail(j, kw)) {
             ok = false;
             break;
@@ -666,6 +755,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
           tmem_wait_st();
           tc_fence_before();
           warp_arrive(&my_pfull[j & 1]);
+          m = m_use;
           continue;
         }
       }
@@ -689,21 +779,13 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         lim = int(min(int64_t(bi.kv_len) - 1, int64_t(i) + band_d + p.band_next));
         lim_lo = int(max(int64_t(0), int64_t(i) + band_d - p.band_pre));
       }
-      if (MODE == kWindow) {
-        // keys of the row: [0, sink) and [lim_lo, lim]; in one tile either
-        // part may be empty, so the sinks become an end of their own
-        lim = int(min(int64_t(bi.kv_len) - 1, int64_t(i) + win_d));
-        lim_lo = int(max(int64_t(0), int64_t(i) + win_d - p.band_pre));
-      }
-      const int sink_end = MODE == kWindow ? min(p.sink, lim + 1) : 0;
       auto hidden = [&](int key) -> bool {
         if (MODE == kPrefix) return key >= p_end;
-        if (MODE == kWindow) return key > lim || (key < lim_lo && key >= sink_end);
         return key > lim || (kBanded && key < lim_lo);
       };
+      // (kWindow: a tile that needs a mask has gone the other way)
       const bool need_mask = (MODE == kPrefix && kv0 + kTileN > p_end) ||
-                             (MODE == kWindow && (kv0 + kTileN - 1 > lim || (kv0 < lim_lo && kv0 + kTileN > sink_end))) ||
-                             (MODE != kPrefix && ragged) || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
+                             (MODE != kPrefix && MODE != kWindow && ragged) || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
                              (kBanded && (kv0 + kTileN - 1 > lim || kv0 < lim_lo)) ||
                              (MODE == kMask && (mb[0] | mb[1] | mb[2] | mb[3]) != 0u);
       float a[8];
@@ -772,17 +854,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       l = l * alpha + (s0 + s1);
       // O_t holds P_t(j-1) V already: Q_t K(j)^T, whose S this thread just
       // read, was issued after that P V on the same tensor pipe.
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-        for (int c = 0; c < DV / 16; ++c) {
-          uint32_t u[16];
-          tmem_ld16(tmem + lane_off + col_o + c * 16, u);
-          tmem_wait_ld(u);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-          tmem_st16(tmem + lane_off + col_o + c * 16, u);
-        }
-      }
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
       // (a prefix ends with a page, and what follows in its tile is zeros)
       if (MODE != kPrefix && ragged && (t == 0 || j >= na) && !clear_v_tail(j, kv0)) {
         ok = false;
