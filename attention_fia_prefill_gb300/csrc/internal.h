@@ -45,11 +45,9 @@ struct WorkItem {
 // i + d - pre <= j <= i + d + next, d = kv_len - q_len of the batch.
 // kMask: an explicit atten_mask (sparse_mode 0 with a mask, 1), key j of row i
 // allowed when mask[i][j] == 0 and i - pre <= j <= i + next (mode 1: no band).
-// kWindow: key j of row i allowed when j <= i + d and (j >= i + d - pre or
-// j < sink), d as for kBand; lengths in device memory, no items.
 // kPrefix: the rows of a whole decode batch over the keys of its shared prefix,
 // cut into splits that leave partial results.
-enum PrefillMode : int { kDense = 0, kCausal = 1, kBlockSparse = 2, kBand = 3, kMask = 4, kWindow = 5, kPrefix = 6 };
+enum PrefillMode : int { kDense = 0, kCausal = 1, kBlockSparse = 2, kBand = 3, kMask = 4, kPrefix = 5 };
 
 struct PrefillParams {
   // 4-D maps (D, S, N, B); TND uses (D, T, N, 1).  With a paged cache the K/V
@@ -94,8 +92,9 @@ struct PrefillParams {
   const float* fp8_vscale;
   int fp8_nqs, fp8_nks;
   DevStatus status;
-  // kWindow: sinks, and lengths as device int32 vectors (nullptr: s1 / s2 for
-  // every batch; a TND query's, and a TND key's, are running sums)
+  // prefill_window.cu: sinks, and lengths as device int32 vectors (nullptr: s1 /
+  // s2 for every batch; a TND query's, and a TND key's, are running sums); n_items
+  // = pairs of tiles x heads, batches, items and band_next not used
   int sink;
   const int32_t* q_lens;
   const int32_t* kv_lens;

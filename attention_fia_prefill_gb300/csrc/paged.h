@@ -65,6 +65,9 @@ struct SpanParams {
 
 cudaError_t launch_block_table(const TableParams& p, cudaStream_t s);
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t s);
+// Window prefill (PrefillParams of an item per pair of tiles and head, lengths
+// on the device).
+cudaError_t launch_prefill_window(const PrefillParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s);
 cudaError_t launch_span_decode(const SpanParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s);
 
 }  // namespace fia

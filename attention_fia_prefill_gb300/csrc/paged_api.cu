@@ -243,7 +243,7 @@ fia_status window_prefill(const fia_tensor* q, const fia_tensor* k, const fia_te
   p.lse_ss = tnd ? w.N1 : 1;
   // pairs of query tiles: TND has at most one part-filled pair a batch
   const int64_t pairs = tnd ? w.S1 / (2 * kTileM) + std::min(w.B, w.S1) : w.B * ((w.S1 + 2 * kTileM - 1) / (2 * kTileM));
-  if (pairs * w.N1 > kMaxInt) return fail(FIA_ERR_SHAPE, "query is too large");
+  if (pairs * w.N1 > kMaxKeys) return fail(FIA_ERR_SHAPE, "query is too large");
   p.n_items = int(pairs * w.N1);
   p.num_heads = int(w.N1);
   p.num_kv_heads = int(w.N2);
@@ -459,8 +459,7 @@ fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor* key, co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_check(profiled(s,
                              [&] {
-                               return launch_prefill_pair(p, int(w.D), int(w.D), query->dtype == FIA_DTYPE_BF16,
-                                                          kWindow, s);
+                               return launch_prefill_window(p, int(w.D), query->dtype == FIA_DTYPE_BF16, sm_count(), s);
                              }),
                     "window prefill launch");
 }

@@ -25,12 +25,6 @@
 // TMEM columns: S_A [0,128), S_B [128,256), O_A [256, 256+DV), O_B [256+DV,
 // 256+2DV).  Causal: tile B needs the K/V tiles of tile A plus at most one; the
 // CTA walks tile B's range and tile A stops early.
-// Window with sinks (kWindow): the band's tiles up to the diagonal, and before
-// them the tiles of the sinks that the band does not hold.  Lengths are read on
-// the device: a CTA finds its batch and rows from its index (TND: by a scan of
-// the running sums), so the launch depends on sizes alone.  Tile B shares tile
-// A's walk, whose first band tile lies before tile B's window: a warp whose
-// rows see nothing of a tile writes P = 0 and skips its softmax.
 // Shared prefix (kPrefix): the rows are a decode batch's, 128 / (heads of a
 // group x new tokens) sequences to a tile, gathered by one 5-D box; the walk is
 // one split of the prefix's tiles (a 128-key tile may take several pages), and
@@ -123,62 +117,6 @@ __device__ __forceinline__ int tiles_for_rows(const BatchInfo& bi, int qa, int m
   return maxkey >= 0 ? maxkey / kTileN + 1 : 0;
 }
 
-// kWindow: the CTA's item from its index.  CTAs run head by head over one pair
-// of tiles (the heads of a group read the same keys), the last pair of a batch
-// first (it sees most keys).  Every warp does the same scan.  Lengths are taken
-// into their tensors' range, whatever they hold.  False: no rows for this CTA.
-__device__ __forceinline__ bool locate_item(const PrefillParams& p, WorkItem& it, BatchInfo& bi) {
-  const int lane = threadIdx.x & 31;
-  const int x = blockIdx.x / p.num_heads;
-  it.h = blockIdx.x - x * p.num_heads;
-  it.cost = 0;
-  constexpr int kRows = 2 * kTileM;
-  if (!p.is_tnd) {
-    const int nt = (p.s1 + kRows - 1) / kRows;
-    it.b = x / nt;
-    it.q_tile = nt - 1 - (x - it.b * nt);
-    bi.q_start = 0;
-    bi.q_len = p.q_lens == nullptr ? p.s1 : min(max(p.q_lens[it.b], 0), p.s1);
-  } else {
-    int before = 0;
-    it.b = -1;
-    for (int b0 = 0; b0 < p.n_batch; b0 += 32) {
-      const int b = b0 + lane;
-      const int s = b < p.n_batch && b > 0 ? min(max(p.q_lens[b - 1], 0), p.s1) : 0;
-      const int e = b < p.n_batch ? min(max(p.q_lens[b], s), p.s1) : s;
-      const int mine = (e - s + kRows - 1) / kRows;
-      int sum = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, x < before + sum);
-      if (hit != 0u) {
-        const int l = __ffs(hit) - 1;
-        it.b = b0 + l;
-        it.q_tile = __shfl_sync(0xffffffffu, before + sum, l) - 1 - x;
-        bi.q_start = __shfl_sync(0xffffffffu, s, l);
-        bi.q_len = __shfl_sync(0xffffffffu, e - s, l);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (it.b < 0) return false;
-  }
-  bi.kv_start = 0;
-  if (p.kv_lens == nullptr) {
-    bi.kv_len = p.s2;
-  } else if (p.is_tnd && p.block_table == nullptr) {
-    const int s = it.b > 0 ? min(max(p.kv_lens[it.b - 1], 0), p.s2) : 0;
-    bi.kv_start = s;
-    bi.kv_len = min(max(p.kv_lens[it.b], s), p.s2) - s;
-  } else {
-    bi.kv_len = min(max(p.kv_lens[it.b], 0), p.s2);
-  }
-  return true;
-}
-
 template <int DQK, int DV, bool BF16, int MODE>
 __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_constant__ PrefillParams p) {
   using C = PairCfg<DQK, DV, MODE == kMask>;
@@ -219,9 +157,6 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
     bi.kv_len = p.s2;
     // rows in tile space: every tile has 128
     bi.q_len = ((p.n_batch + p.tile_batches - 1) / p.tile_batches) * kTileM;
-  } else if constexpr (MODE == kWindow) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) status_stamp(p.status);   // also when the CTA has no rows
-    if (!locate_item(p, it, bi)) return;
   } else {
     it = p.items[blockIdx.x];
     bi = p.batches[it.b];
@@ -274,44 +209,16 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       nb = has_b ? max(na, lb < 0 ? 0 : lb - first + 1) : 0;
     }
   }
-  // window with sinks: the band's tiles as above with nothing past the
-  // diagonal, n_sink tiles of sinks before them
-  int n_sink = 0;
-  const int64_t win_d = MODE == kWindow ? int64_t(bi.kv_len) - bi.q_len : 0;
-  if (MODE == kWindow) {
-    const int64_t lo = max(int64_t(0), q0 + win_d - p.band_pre);
-    const int64_t hi_a = min(q0 + kTileM, bi.q_len) - 1 + win_d, hi = min(q0 + 2 * kTileM, bi.q_len) - 1 + win_d;
-    jt0 = int(lo / kTileN);
-    const bool rows = q0 < bi.q_len && hi >= 0;   // hi < kv_len, hi >= lo
-    n_sink = rows ? min((p.sink + kTileN - 1) / kTileN, jt0) : 0;
-    na = rows && hi_a >= 0 ? n_sink + int(hi_a / kTileN) - jt0 + 1 : 0;
-    nb = rows && has_b ? n_sink + int(hi / kTileN) - jt0 + 1 : 0;
-  }
   if (MODE == kPrefix) {
     const int tiles = (p.s2 + kTileN - 1) / kTileN;
     jt0 = int(int64_t(tiles) * it.cost / p.n_splits);
     na = int(int64_t(tiles) * (it.cost + 1) / p.n_splits) - jt0;
     nb = has_b ? na : 0;
   }
-  // window with sinks: the columns a product takes of its tile, a multiple of
-  // 16: those of the sinks in the last tile before the band, and in tile B's
-  // first band tile when its window starts past it; else all 128
-  int cols_sink = kTileN, cols_b = kTileN;
-  if (MODE == kWindow) {
-    auto sinks_of = [&](int tile) -> int { return min((max(p.sink - tile * kTileN, 1) + 15) & ~15, kTileN); };
-    cols_sink = sinks_of(max(n_sink - 1, 0));
-    if (int64_t(jt0 + 1) * kTileN <= q0 + kTileM + win_d - p.band_pre) cols_b = sinks_of(jt0);
-  }
-  auto columns = [&](int t, int j) -> int {
-    if (MODE != kWindow) return kTileN;
-    return j == n_sink - 1 ? cols_sink : (t == 1 && j == n_sink) ? cols_b : kTileN;
-  };
-  // K/V tile of the walk's step j
-  auto tile_of = [&](int j) -> int { return MODE == kWindow ? (j < n_sink ? j : jt0 + j - n_sink) : jt0 + j; };
   const int nl = max(na, nb);
 
   if (threadIdx.x == 0) {
-    if (MODE != kWindow && blockIdx.x == 0) status_stamp(p.status);
+    if (blockIdx.x == 0) status_stamp(p.status);
     mbar_init(q_full, 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
@@ -366,16 +273,16 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
             tma_load_5d(smem + C::kOffQ + t * C::kTileQK + c * C::kBoxBytes, &p.tm_q, q_full, c * 64, 0, 0, kvh,
                         (2 * it.q_tile + t) * p.tile_batches);
       } else {
-      mbar_arrive_expect_tx(q_full, 2 * C::kTileQK);
+        mbar_arrive_expect_tx(q_full, 2 * C::kTileQK);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int c = 0; c < C::kChunksQK; ++c) {
-          int col;
-          const CUtensorMap* m = qk_src(c, &p.tm_q, &p.tm_qr, col);
-          tma_load_4d(smem + C::kOffQ + t * C::kTileQK + c * C::kBoxBytes, m, q_full, col, q_row0 + t * kTileM, it.h,
-                      b_coord);
-        }
+          for (int c = 0; c < C::kChunksQK; ++c) {
+            int col;
+            const CUtensorMap* m = qk_src(c, &p.tm_q, &p.tm_qr, col);
+            tma_load_4d(smem + C::kOffQ + t * C::kTileQK + c * C::kBoxBytes, m, q_full, col, q_row0 + t * kTileM, it.h,
+                        b_coord);
+          }
       }
       // one 128-key tile of a paged prefix, page by page (a page id outside
       // the pool, or past the prefix, reads as zeros)
@@ -394,7 +301,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         const int sk = j % KS, sv = j % VS;
         // K/V tile coordinates: (row, batch) of a contiguous tensor, or (row in
         // block, block id) of a paged pool (the table read overlaps the wait)
-        const int key = tile_of(j) * kTileN;
+        const int key = (jt0 + j) * kTileN;
         int kv_r = kv_row0 + key, kv_b = b_coord;
         if (MODE != kPrefix && p.block_table != nullptr) {
           kv_b = __ldg(p.block_table + int64_t(it.b) * p.table_stride + key / p.block_size);
@@ -455,7 +362,6 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, BF16 ? 1 : 0, 0, 0);
-      constexpr uint32_t idesc_qk0 = idesc_f16(128, 0, BF16 ? 1 : 0, 0, 0);   // without its N
       constexpr uint32_t idesc_pv = idesc_f16(128, DV, BF16 ? 1 : 0, 0, 1);
       // Descriptors of every operand buffer, built once; an MMA's K-slice
       // only moves the start address (bits 0..13, in 16-byte units), which
@@ -479,11 +385,10 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         const uint64_t qd = t == 0 ? qd0 : qd1;
         const uint64_t kd = kd0 + uint64_t(s) * kStepK;
         const uint32_t dst = tmem + t * 128;
-        const uint32_t idesc = MODE == kWindow ? idesc_qk0 | (uint32_t(columns(t, j)) >> 3 << 17) : idesc_qk;
 #pragma unroll
         for (int kk = 0; kk < DQK / 16; ++kk) {
           const uint64_t off = uint64_t(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
-          mma_ss(dst, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
+          mma_ss(dst, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
         }
         mma_commit(&s_full[3 * t + s]);
         last_bar = &s_full[3 * t + s];
@@ -501,15 +406,9 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         const uint64_t vd = vd0 + uint64_t(s) * kStepV;
         const uint32_t dst = tmem + C::kColO + t * DV;
         const uint32_t pt = tmem + t * 128;
-        const int cols = columns(t, j);
-        if (MODE != kWindow || cols == kTileN) {
 #pragma unroll
-          for (int kk = 0; kk < kTileN / 16; ++kk)
-            mma_ts(dst, pt + kk * 8, vd + uint64_t((kk * 2048) >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-        } else {
-          for (int kk = 0; kk < cols / 16; ++kk)
-            mma_ts(dst, pt + kk * 8, vd + uint64_t((kk * 2048) >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < kTileN / 16; ++kk)
+          mma_ts(dst, pt + kk * 8, vd + uint64_t((kk * 2048) >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
         if (t == 0 && nb > 0) {
           if (j == na - 1) {
             mma_commit(pva_done);
@@ -614,20 +513,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       ph = r % p.group;
       if (pb < p.n_batch) p_end = min(max(max(p.kv_lens[pb], 0) - p.q_tokens + pt + 1, 0), p.s2);
     }
-    // kWindow: the row's position (lengths and pre are at most 2^30)
-    const int w_pos = MODE == kWindow ? i + int(win_d) : 0;
     const bool warp_rows = MODE != kPrefix || __any_sync(0xffffffffu, pb < p.n_batch);
-    auto rescale_o = [&](float alpha) {
-#pragma unroll 1
-      for (int c = 0; c < DV / 16; ++c) {
-        uint32_t u[16];
-        tmem_ld16(tmem + lane_off + col_o + c * 16, u);
-        tmem_wait_ld(u);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-        tmem_st16(tmem + lane_off + col_o + c * 16, u);
-      }
-    };
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -682,83 +568,6 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         warp_arrive(&my_pfull[j & 1]);
         continue;
       }
-      if constexpr (MODE == kWindow) {
-        const int kw = tile_of(j) * kTileN;
-        // the first and the last row's last key and window
-        const int pos_0 = w_pos - lane, pos_31 = pos_0 + 31;
-        const int lim_0 = min(bi.kv_len - 1, pos_0), lim_31 = min(bi.kv_len - 1, pos_31);
-        const int lo_0 = pos_0 - p.band_pre, lo_31 = pos_31 - p.band_pre;
-        if (kw + kTileN - 1 > lim_0 || kw < lo_31) {
-          // A tile on an edge of the warp's rows, 32 columns at a time: those
-          // that no row sees are neither loaded nor exponentiated (P = 0).  Two
-          // passes over S, so that this path needs few registers: masks in the
-          // full tiles' path below cost it a quarter of its speed.
-          auto hid = [&](int k0) -> bool { return k0 > lim_31 || (k0 >= p.sink && k0 + 31 < lo_0); };
-          // columns [0, sinks) and [from, to] of the piece are the row's
-          auto piece = [&](int q, uint32_t (&su)[32]) {
-            tmem_ld32(tmem + lane_off + col_s + 32 * q, su);
-            const int k0 = kw + 32 * q, to = min(bi.kv_len - 1, w_pos) - k0, from = w_pos - p.band_pre - k0;
-            const int sinks = min(p.sink - k0, to + 1);
-            tmem_wait_ld(su);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e > to || (e < from && e >= sinks)) su[e] = __float_as_uint(-INFINITY);
-          };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            if (hid(kw + 32 * q)) continue;
-            uint32_t su[32];
-            piece(q, su);
-            float a[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] = fmaxf(__uint_as_float(su[k]), __uint_as_float(su[4 + k]));
-#pragma unroll
-            for (int c = 8; c < 32; c += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) a[k] = fmax3(a[k], __uint_as_float(su[c + k]), __uint_as_float(su[c + 4 + k]));
-            top = fmax3(top, fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-          }
-          const float m_new = fmaxf(m, top * sl2);
-          const float m_use = (m == -INFINITY || m_new > m + 8.f) ? m_new : m;   // as below
-          const float alpha = (m_use == m) ? 1.f : fast_exp2(m - m_use);
-          const float mo = (m_use == -INFINITY) ? 0.f : m_use;
-          uint64_t acc2[2] = {0ull, 0ull};   // summed in the full tiles' order
-          // (P of a piece takes columns of pieces that have been read)
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t u[16];
-            if (hid(kw + 32 * q)) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = 0u;
-            } else {
-              uint32_t su[32];
-              piece(q, su);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float y0 = fast_exp2(fmaf(__uint_as_float(su[2 * e]), sl2, -mo));
-                const float y1 = fast_exp2(fmaf(__uint_as_float(su[2 * e + 1]), sl2, -mo));
-                acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(y0, y1));
-                u[e] = pack2(y0, y1, BF16);
-              }
-            }
-            tmem_st16(tmem + lane_off + col_s + q * 16, u);
-          }
-          float s0, s1;
-          f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
-          l = l * alpha + (s0 + s1);
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
-          if (kw + kTileN > bi.kv_len && (t == 0 || j >= na) && !clear_v_tail(j, kw)) {
-            ok = false;
-            break;
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          warp_arrive(&my_pfull[j & 1]);
-          m = m_use;
-          continue;
-        }
-      }
       // S in two halves: the second half's load is in flight while the
       // first half is masked and reduced.
       uint32_t su[4][32];
@@ -769,7 +578,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       tmem_ld32(tmem + lane_off + col_s + 64, su[2]);
       tmem_ld32(tmem + lane_off + col_s + 96, su[3]);
       float* x = reinterpret_cast<float*>(&su[0][0]);
-      const int kv0 = tile_of(j) * kTileN;
+      const int kv0 = (jt0 + j) * kTileN;
       const bool ragged = kv0 + kTileN > bi.kv_len;
       // keys allowed for this row: [lim_lo, lim]
       int lim = (MODE == kCausal) ? min(bi.kv_len - 1, diag) : bi.kv_len - 1;
@@ -783,9 +592,8 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         if (MODE == kPrefix) return key >= p_end;
         return key > lim || (kBanded && key < lim_lo);
       };
-      // (kWindow: a tile that needs a mask has gone the other way)
       const bool need_mask = (MODE == kPrefix && kv0 + kTileN > p_end) ||
-                             (MODE != kPrefix && MODE != kWindow && ragged) || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
+                             (MODE != kPrefix && ragged) || (MODE == kCausal && kv0 + kTileN - 1 > tile_q0 + diag_off) ||
                              (kBanded && (kv0 + kTileN - 1 > lim || kv0 < lim_lo)) ||
                              (MODE == kMask && (mb[0] | mb[1] | mb[2] | mb[3]) != 0u);
       float a[8];
@@ -854,7 +662,17 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       l = l * alpha + (s0 + s1);
       // O_t holds P_t(j-1) V already: Q_t K(j)^T, whose S this thread just
       // read, was issued after that P V on the same tensor pipe.
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < DV / 16; ++c) {
+          uint32_t u[16];
+          tmem_ld16(tmem + lane_off + col_o + c * 16, u);
+          tmem_wait_ld(u);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+          tmem_st16(tmem + lane_off + col_o + c * 16, u);
+        }
+      }
       // (a prefix ends with a page, and what follows in its tile is zeros)
       if (MODE != kPrefix && ragged && (t == 0 || j >= na) && !clear_v_tail(j, kv0)) {
         ok = false;
@@ -893,9 +711,8 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         }
       }
     } else if (ok) {
-      // (kWindow: the padding rows of a padded layout are this CTA's to write)
-      const bool row_valid = i < (MODE == kWindow && !is_tnd ? p.s1 : bi.q_len);
-      const bool has = MODE == kWindow ? l != 0.f && i < bi.q_len : l > 0.f;
+      const bool row_valid = i < bi.q_len;
+      const bool has = l > 0.f;
       const float inv_l = has ? 1.f / l : 0.f;
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       T* orow = reinterpret_cast<T*>(p.out) + (is_tnd ? int64_t(bi.q_start + i) * p.out_ss
@@ -968,13 +785,6 @@ cudaError_t launch_mask_tile_summary(const uint8_t* mask, int64_t s1, int64_t s2
 cudaError_t launch_prefill_pair(const PrefillParams& p, int head_dim_qk, int head_dim_v, bool bf16, int mode,
                                 cudaStream_t s) {
   if (p.n_items == 0) return cudaSuccess;
-  if (mode == kWindow) {
-    if (head_dim_qk == 128 && head_dim_v == 128)
-      return bf16 ? launch_pair_one<128, 128, true, kWindow>(p, s) : launch_pair_one<128, 128, false, kWindow>(p, s);
-    if (head_dim_qk == 64 && head_dim_v == 64)
-      return bf16 ? launch_pair_one<64, 64, true, kWindow>(p, s) : launch_pair_one<64, 64, false, kWindow>(p, s);
-    return cudaErrorInvalidValue;
-  }
   if (mode == kPrefix) {
     if (head_dim_qk == 128 && head_dim_v == 128)
       return bf16 ? launch_pair_one<128, 128, true, kPrefix>(p, s) : launch_pair_one<128, 128, false, kPrefix>(p, s);
