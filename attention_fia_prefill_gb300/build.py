@@ -63,7 +63,7 @@ def _ext_commands(cc):
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
     return ([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{i}" for i in inc), "-c", EXT_SOURCE, "-o", obj],
             [cxx, "-shared", "-o", EXT + ".tmp", obj, "-L" + OUT_DIR, "-lfia", "-L" + lib, "-ltorch_python", "-ltorch_cpu",
-             "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
+             "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
 
 
 def _run(cmd, what, verbose=False):

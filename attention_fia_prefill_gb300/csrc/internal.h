@@ -25,6 +25,23 @@ cudaError_t set_smem_once(int bytes) {
   return e;
 }
 
+// Launch with programmatic stream serialisation: the grid may start while the
+// kernel before it on the stream ends, and waits for it with grid_dep_wait().
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 constexpr int kTileM = 128;   // query rows per prefill CTA
 constexpr int kTileN = 128;   // keys per KV tile
 

@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(kTableThreads) block_table_kernel(const TableP
   __shared__ int s_cu[kTableChunk];        // new tokens up to and with the request, within the chunk
   __shared__ int s_ctx[kTableChunk];
   __shared__ int64_t s_blk[kTableChunk];   // blocks asked for before the request
+  grid_dep_launch();
+  grid_dep_wait();   // the kernel before this one is complete: its writes are read, what it reads may be written
   const uint32_t bs = uint32_t(p.block_size);
   const int64_t t0 = int64_t(blockIdx.x) * kTableChunk;
   const int64_t t1 = min(t0 + kTableChunk, int64_t(p.n_tokens));
@@ -157,6 +159,8 @@ __global__ void __launch_bounds__(kTableThreads) block_table_kernel(const TableP
 __global__ void __launch_bounds__(256) cache_write_kernel(const CacheWriteParams p) {
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int y = blockIdx.y, lane = threadIdx.x & 31;
+  grid_dep_launch();
+  grid_dep_wait();
   if (t >= p.n_tokens) return;
   const int slot = p.slots[t];
   if (slot < 0 || slot >= p.n_slots) return;
@@ -185,14 +189,12 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheWriteParams
 
 cudaError_t launch_block_table(const TableParams& p, cudaStream_t s) {
   const unsigned grid = unsigned(std::max<int64_t>(1, (int64_t(p.n_tokens) + kTableChunk - 1) / kTableChunk));
-  block_table_kernel<<<grid, kTableThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(block_table_kernel, dim3(grid), kTableThreads, 0, s, p);
 }
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t s) {
   const dim3 grid(unsigned((int64_t(p.n_tokens) + 7) / 8), p.vecs[1] > 0 ? 2u : 1u);
-  cache_write_kernel<<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(cache_write_kernel, grid, 256, 0, s, p);
 }
 
 }  // namespace fia

@@ -146,7 +146,11 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
   WorkItem it;
   BatchInfo bi;
   if constexpr (MODE == kPrefix) {
-    grid_dep_launch();   // the decode of the sequences' own keys needs no result of this kernel before its join
+    // The decode of the sequences' own keys needs no result of this kernel
+    // before its join, but what came before both has to be complete: it is let
+    // go after the wait.
+    grid_dep_wait();
+    grid_dep_launch();
     // splits outermost: the pairs of rows that read the same keys are neighbours
     const int x = blockIdx.x / p.n_pairs;
     it.cost = x / p.num_kv_heads;                  // the split
@@ -767,6 +771,7 @@ cudaError_t launch_pair_one(const PrefillParams& p, cudaStream_t s) {
   constexpr int smem = MODE == kMask ? C::kSmemMask : C::kSmem;
   cudaError_t e = set_smem_once<prefill_pair_kernel<DQK, DV, BF16, MODE>>(smem);
   if (e != cudaSuccess) return e;
+  if (MODE == kPrefix) return launch_early(k, dim3(unsigned(p.n_items)), C::kThreads, smem, s, p);
   k<<<p.n_items, C::kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }

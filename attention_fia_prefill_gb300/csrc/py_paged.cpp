@@ -8,8 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -120,8 +119,10 @@ struct Desc {
   const fia_tensor* ptr() const { return here ? &d : nullptr; }
 };
 
+// (the allocator called directly: through torch's dispatcher an output costs
+// twice as much host time)
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType t, c10::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(t).device(dev));
+  return at::detail::empty_cuda(shape, t, dev, std::nullopt);
 }
 
 // An output argument: the caller's, or a new one of this shape and type.
@@ -159,7 +160,7 @@ struct Attention {
     prm.pre_tokens = c.integer(i + 4);
     prm.block_size = c.integer(i + 5);
     prm.softmax_lse_flag = c.truth(i + 6) ? 1 : 0;
-    out = c.none(i + 7) ? at::empty_like(q) : c.tensor(i + 7, "out");
+    out = c.none(i + 7) ? empty(q.sizes(), q.scalar_type(), *c.device) : c.tensor(i + 7, "out");
     out_d.set(out, "out");
     if (!c.none(i + 8)) {
       lse = c.tensor(i + 8, "softmax_lse");

@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
 
   grid_dep_launch();
   cluster_arrive();   // (waited for before the join's first remote store: every CTA runs by then)
-  // Behind a prefix kernel (an ordinary launch, so everything before it is
-  // complete) only the join has to wait for it.
+  // Behind a prefix kernel, which lets this one go once everything before both
+  // is complete, only the join has to wait for it.
   if (p.n_parts == 0) grid_dep_wait();
 
   // ---------------------------------------------------------------- Q
