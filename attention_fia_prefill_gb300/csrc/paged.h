@@ -61,6 +61,10 @@ struct SpanParams {
   const float2* part_ml;
   int n_parts;
   int64_t part_rows;              // rows of one part
+  // set by the launch: CTAs of a unit (log2), log2 of block_size (-1: no power
+  // of two), 2^16 / q_tokens
+  int lg_cs, lg_block;
+  uint32_t q_inv;
 };
 
 cudaError_t launch_block_table(const TableParams& p, cudaStream_t s);

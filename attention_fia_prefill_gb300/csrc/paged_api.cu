@@ -102,7 +102,8 @@ fia_status span_params(const fia_tensor* q, const fia_tensor* k, const fia_tenso
   if (!same_shape(k, v)) return fail(FIA_ERR_SHAPE, "key and value shapes differ");
   if (!aligned16(q->data) || !aligned16(k->data) || !aligned16(v->data) || !aligned16(out->data))
     return fail(FIA_ERR_ALIGNMENT, "query/key/value/attention_out must be 16-byte aligned");
-  if (B * N2 > kMaxInt / 16) return fail(FIA_ERR_SHAPE, "B x KV_N = %lld is too large", (long long)(B * N2));
+  if (B > kMaxInt / 16 || N2 > 65535)
+    return fail(FIA_ERR_SHAPE, "B = %lld or KV_N = %lld is too large", (long long)B, (long long)N2);
   int64_t S2;
   if (present(table)) {
     if (table->dtype != FIA_DTYPE_I32 || table->ndim != 2 || table->shape[0] != B)

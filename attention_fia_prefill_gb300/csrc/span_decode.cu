@@ -62,7 +62,7 @@ struct SpanCfg {
   // share of the unit's float4s, and their (max, sum) of every row
   static constexpr int kOffML = kRing;
   static constexpr int kOffIn = kOffML + kGroups * 16 * MT * 8;
-  static constexpr int kOffInML = kOffIn + (16 * MT * (D / 4) + kMostCtas) * 16;
+  static constexpr int kOffInML = kOffIn + (16 * MT * (D / 4) + 8 * kMostCtas) * 16;
   static constexpr int kSmem = kOffInML + kMostCtas * 16 * MT * 8 + 128;
 };
 
@@ -95,16 +95,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
 }
 // The cluster's barrier in halves: arrive releases this thread's writes, wait
 // acquires every CTA's.
@@ -140,9 +130,12 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rt = warp % MT, kg = warp / MT;
   const int fg = lane >> 2, ft = lane & 3;
-  const uint32_t cs = cluster_size(), rank = cluster_rank();
-  const int unit = blockIdx.x / cs;
-  const int b = unit / p.N2, kvh = unit - b * p.N2;
+  // grid: (batch x CTA of the unit, kv head).  Divisions by run-time numbers are
+  // kept out of the kernel's start and end, which run once from a cold
+  // instruction cache: a division is twenty instructions, at ten cycles each.
+  const uint32_t lg = uint32_t(p.lg_cs), cs = 1u << lg, rank = blockIdx.x & (cs - 1u);
+  const int b = int(blockIdx.x >> lg), kvh = blockIdx.y;
+  auto head_of = [&](int r) -> int { return int((uint32_t(r) * p.q_inv) >> 16); };   // r / q_tokens, r < 64
 
   grid_dep_launch();
   cluster_arrive();   // (waited for before the join's first remote store: every CTA runs by then)
@@ -156,8 +149,9 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   // the length, the page ids and the keys, which wait for one another.
   const int r0 = rt * 16 + fg, r1 = r0 + 8;
   const T* qp = static_cast<const T*>(p.q) + int64_t(b) * p.q_sb + 2 * ft;
-  const T* q0 = qp + int64_t(kvh * p.group + r0 / p.q_tokens) * p.q_sn + int64_t(r0 % p.q_tokens) * p.q_ss;
-  const T* q1 = qp + int64_t(kvh * p.group + r1 / p.q_tokens) * p.q_sn + int64_t(r1 % p.q_tokens) * p.q_ss;
+  const int h0 = head_of(r0), h1 = head_of(r1), tk0 = r0 - h0 * p.q_tokens, tk1 = r1 - h1 * p.q_tokens;
+  const T* q0 = qp + (kvh * p.group + h0) * p.q_sn + tk0 * p.q_ss;
+  const T* q1 = qp + (kvh * p.group + h1) * p.q_sn + tk1 * p.q_ss;
   uint32_t qa[KK][4];
 #pragma unroll
   for (int kk = 0; kk < KK; ++kk) {
@@ -196,7 +190,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   auto start_of = [&](int q) -> int64_t {
     const int j = tile_key(q / SUB, q % SUB);
     if (p.block_table == nullptr) return int64_t(b) * p.blk_stride + int64_t(j) * p.row_stride;
-    const int page = j / p.block_size;
+    const int page = p.lg_block >= 0 ? j >> p.lg_block : j / p.block_size;
     if (page >= p.table_stride) return -1;
     const int id = p.block_table[int64_t(b) * p.table_stride + page];
     if (id < 0 || id >= p.n_blocks) return -1;
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   };
   for (int i = 0; i < ST - 1; ++i) issue(i);
 
-  const int p0 = first + r0 % p.q_tokens, p1 = first + r1 % p.q_tokens;   // the rows' positions
+  const int p0 = first + tk0, p1 = first + tk1;   // the rows' positions
   const int w0 = int(max(int64_t(p0) - p.pre, int64_t(0))), w1 = int(max(int64_t(p1) - p.pre, int64_t(0)));
   const int win_last = int(max(int64_t(L) - 1 - p.pre, int64_t(0)));   // the last token's window
   auto sees = [&](int pos, int w, int j) -> bool { return j <= pos && j >= p.base && (j < p.sink || j >= w); };
@@ -379,9 +373,9 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   }
   __syncthreads();
   // This CTA's groups joined, float4 by float4, each sent to the CTA that
-  // writes it: CTA k of the cluster has items [k share, (k + 1) share).
+  // writes it: the CTAs of the cluster take eight in turn.
   const int items = p.rows * (D / 4);
-  const int share = (items + int(cs) - 1) / int(cs);
+  const int share = ((items + 8 * int(cs) - 1) >> (3 + lg)) << 3;
   const uint32_t in_o = smem_u32(smem + C::kOffIn), in_ml = smem_u32(smem + C::kOffInML);
   __syncwarp();
   cluster_wait();
@@ -400,8 +394,8 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
       l += w * w2.y;
       a.x += w * x.x; a.y += w * x.y; a.z += w * x.z; a.w += w * x.w;
     }
-    const int owner = e / share;
-    st_peer4(peer_addr(in_o + (rank * share + e - owner * share) * 16, owner), a);
+    const int owner = (e >> 3) & int(cs - 1u), slot = ((e >> (3 + lg)) << 3) + (e & 7);
+    st_peer4(peer_addr(in_o + (rank * share + slot) * 16, owner), a);
     if (c4 == 0)
       for (uint32_t k = 0; k < cs; ++k) st_peer2(peer_addr(in_ml + (rank * 16 * MT + r) * 8, k), make_float2(top, l));
   }
@@ -412,10 +406,10 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   const float4* xo = reinterpret_cast<const float4*>(smem + C::kOffIn);
   const float2* xml = reinterpret_cast<const float2*>(smem + C::kOffInML);
   for (int i = threadIdx.x; i < share; i += kSpanThreads) {
-    const int e = int(rank) * share + i;
+    const int e = ((((i >> 3) << lg) + int(rank)) << 3) + (i & 7);
     if (e >= items) break;
     const int r = e / (D / 4), c4 = e % (D / 4);
-    const int head = kvh * p.group + r / p.q_tokens, tokn = r % p.q_tokens;
+    const int h = head_of(r), head = kvh * p.group + h, tokn = r - h * p.q_tokens;
     float top = -INFINITY;
     for (uint32_t g = 0; g < cs; ++g) top = fmaxf(top, xml[g * 16 * MT + r].x);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -475,7 +469,7 @@ cudaError_t launch_one(const SpanParams& p, int cs, cudaStream_t s) {
   cudaError_t e = set_smem_once<span_decode_kernel<D, BF16, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.B * p.N2 * cs));
+  cfg.gridDim = dim3(unsigned(p.B * cs), unsigned(p.N2));
   cfg.blockDim = dim3(kSpanThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -512,11 +506,17 @@ int cluster_ctas(int64_t units, int64_t tiles, int groups, bool even, int64_t sl
 
 }  // namespace
 
-cudaError_t launch_span_decode(const SpanParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s) {
+cudaError_t launch_span_decode(const SpanParams& params, int head_dim, bool bf16, int n_sm, cudaStream_t s) {
+  SpanParams p = params;
   const int mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
   const int64_t span = std::min<int64_t>(p.kv_max - p.base, int64_t(p.sink) + p.pre + p.q_tokens);
   const int cs = cluster_ctas(int64_t(p.B) * p.N2, span / kSpanTile + 1, 4 / mt,
                               span < p.kv_max - p.base, (head_dim == 64 ? 4 : 2) * n_sm);
+  p.lg_cs = cs == 8 ? 3 : cs / 2;
+  p.q_inv = 65536u / unsigned(p.q_tokens) + 1u;   // floor(r q_inv / 2^16) = r / q_tokens for r < 64, q_tokens <= 16
+  p.lg_block = -1;
+  for (int k = 4; k < 31; ++k)
+    if (p.block_size == 1 << k) p.lg_block = k;
 #define FIA_SPAN(DD, BB)                                    \
   switch (mt) {                                             \
     case 1: return launch_one<DD, BB, 1>(p, cs, s);         \
