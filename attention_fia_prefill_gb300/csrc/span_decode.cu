@@ -138,15 +138,36 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   auto head_of = [&](int r) -> int { return int((uint32_t(r) * p.q_inv) >> 16); };   // r / q_tokens, r < 64
 
   grid_dep_launch();
-  cluster_arrive();   // (waited for before the join's first remote store: every CTA runs by then)
+  if (lg != 0) cluster_arrive();   // (waited for before the join's first remote store: every CTA runs by then)
   // Behind a prefix kernel, which lets this one go once everything before both
   // is complete, only the join has to wait for it.
   if (p.n_parts == 0) grid_dep_wait();
+  // Length, page ids and keys wait for one another: the length first, and
+  // without a window, when they do not depend on it, the page ids; the queries
+  // load meanwhile.
+  int len = p.kv_max;
+  if (p.kv_len != nullptr)
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(len) : "l"(p.kv_len + b) : "memory");
+  const bool gapless = p.pre >= p.kv_max;      // no window: the tiles are t_base, t_base + 1, ...
+  const int t_base = p.base / kSpanTile;
+  const int groups = C::kGroups << lg;
+  const int gi = int(rank) * C::kGroups + kg;
+  // where the tile of keys j.. starts in the caches, in elements; -1: nowhere
+  auto tile_start = [&](int j) -> int64_t {
+    if (p.block_table == nullptr) return int64_t(b) * p.blk_stride + int64_t(j) * p.row_stride;
+    const int page = p.lg_block >= 0 ? j >> p.lg_block : j / p.block_size;
+    if (page >= p.table_stride) return -1;
+    const int id = p.block_table[int64_t(b) * p.table_stride + page];
+    if (id < 0 || id >= p.n_blocks) return -1;
+    return int64_t(id) * p.blk_stride + int64_t(j - page * p.block_size) * p.row_stride;
+  };
+  // (one per lane: those of the group's first 32 tiles)
+  int64_t starts = -1;
+  if (gapless) starts = tile_start((t_base + (gi + lane / SUB * groups) * SUB + lane % SUB) * kSpanTile);
 
   // ---------------------------------------------------------------- Q
   // A fragments of the warp's 16 rows: lane (fg, ft) holds rows fg, fg + 8 at
-  // columns 2 ft, 2 ft + 1 and 8 + 2 ft, 9 + 2 ft of every 16.  Loaded ahead of
-  // the length, the page ids and the keys, which wait for one another.
+  // columns 2 ft, 2 ft + 1 and 8 + 2 ft, 9 + 2 ft of every 16
   const int r0 = rt * 16 + fg, r1 = r0 + 8;
   const T* qp = static_cast<const T*>(p.q) + int64_t(b) * p.q_sb + 2 * ft;
   const int h0 = head_of(r0), h1 = head_of(r1), tk0 = r0 - h0 * p.q_tokens, tk1 = r1 - h1 * p.q_tokens;
@@ -160,24 +181,19 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
     qa[kk][2] = r0 < p.rows ? *reinterpret_cast<const uint32_t*>(q0 + kk * 16 + 8) : 0u;
     qa[kk][3] = r1 < p.rows ? *reinterpret_cast<const uint32_t*>(q1 + kk * 16 + 8) : 0u;
   }
-  const int L = p.kv_len == nullptr ? p.kv_max : min(max(p.kv_len[b], 0), p.kv_max);
+  const int L = min(max(len, 0), p.kv_max);
   const int first = L - p.q_tokens;               // position of token 0 (may be negative: tokens that see nothing)
   // the tiles that hold a key some row may see: the sinks' [base / 16, t_sink)
   // and [t_win, t_end)
   const int t_end = (L + kSpanTile - 1) / kSpanTile;
-  const int t_base = p.base / kSpanTile;
   const int t_sink = min(t_end, max(t_base, (p.sink + kSpanTile - 1) / kSpanTile));
   const int win = int(max(int64_t(first) - p.pre, int64_t(0)));   // first key of token 0's window
   const int t_win = max(t_sink, win / kSpanTile);
   const int n_sink = max(0, t_sink - t_base);
   const int n_tiles = n_sink + max(0, t_end - t_win);
-  const int groups = int(cs) * C::kGroups;
-  const int gi = int(rank) * C::kGroups + kg;
   const int n_steps = (n_tiles + SUB - 1) / SUB;
   const int n = n_steps > gi ? (n_steps - gi + groups - 1) / groups : 0;   // this group's steps
   // First key of tile u of the group's i-th step; past the list it is L or more.
-  // Without a window the list has no gap, and page ids load beside the length.
-  const bool gapless = p.pre >= p.kv_max;
   auto tile_key = [&](int i, int u) -> int {
     const int v = (gi + i * groups) * SUB + u;
     if (gapless) return (t_base + v) * kSpanTile;
@@ -185,18 +201,11 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   };
 
   // ---------------------------------------------------------------- loads
-  // where the group's q-th tile (step q / SUB) starts in the caches, in
-  // elements; -1: nowhere.  32 tiles at a time, one per lane, a batch ahead.
-  auto start_of = [&](int q) -> int64_t {
-    const int j = tile_key(q / SUB, q % SUB);
-    if (p.block_table == nullptr) return int64_t(b) * p.blk_stride + int64_t(j) * p.row_stride;
-    const int page = p.lg_block >= 0 ? j >> p.lg_block : j / p.block_size;
-    if (page >= p.table_stride) return -1;
-    const int id = p.block_table[int64_t(b) * p.table_stride + page];
-    if (id < 0 || id >= p.n_blocks) return -1;
-    return int64_t(id) * p.blk_stride + int64_t(j - page * p.block_size) * p.row_stride;
-  };
-  int64_t starts = start_of(lane), starts_next = -1;
+  // tile_start of the group's q-th tile (step q / SUB): 32 tiles at a time, one
+  // per lane, a batch ahead
+  auto start_of = [&](int q) -> int64_t { return tile_start(tile_key(q / SUB, q % SUB)); };
+  if (!gapless) starts = start_of(lane);
+  int64_t starts_next = -1;
   int batch = 0;
   const uint32_t ring = smem_u32(smem) + kg * ST * C::kStageBytes;
   // this lane's first piece of a tile, and the rows between its pieces
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   const int share = ((items + 8 * int(cs) - 1) >> (3 + lg)) << 3;
   const uint32_t in_o = smem_u32(smem + C::kOffIn), in_ml = smem_u32(smem + C::kOffInML);
   __syncwarp();
-  cluster_wait();
+  if (lg != 0) cluster_wait();
   for (int e = threadIdx.x; e < items; e += kSpanThreads) {
     const int r = e / (D / 4), c4 = e % (D / 4);
     float top = -INFINITY;
@@ -400,9 +409,9 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
       for (uint32_t k = 0; k < cs; ++k) st_peer2(peer_addr(in_ml + (rank * 16 * MT + r) * 8, k), make_float2(top, l));
   }
   __syncwarp();
-  cluster_arrive();
+  if (lg != 0) cluster_arrive();
   if (p.n_parts > 0) grid_dep_wait();   // (by every thread: the prefix's results are in)
-  cluster_wait();                       // nothing of this CTA is read or written by another from here on
+  if (lg != 0) cluster_wait(); else __syncthreads();   // no CTA reads or writes another's memory from here on
   const float4* xo = reinterpret_cast<const float4*>(smem + C::kOffIn);
   const float2* xml = reinterpret_cast<const float2*>(smem + C::kOffInML);
   for (int i = threadIdx.x; i < share; i += kSpanThreads) {
