@@ -274,3 +274,60 @@ def test_timeout_path(fia, op):
     assert status in (0, 10)     # a wait whose first try succeeds does not look at the limit
     again = call()
     assert fia.fia_device_status(ws) == 0 and torch.equal(good, again)
+
+
+# ------------------------------------------------------------------ caches past 2^31 elements
+def test_cache_past_32_bit_offsets(fia):
+    """A pool of 2.6e9 elements (5.2 GB) each for keys and values: rows in its last blocks are written and attended to."""
+    nblk, n2, bs, D, n1, B = 20000, 8, 128, 128, 16, 3
+    kc, vc = (torch.empty(nblk, n2, bs, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    lens = [300, 129, 700]
+    T = sum(lens)
+    x = torch.randn(T, n1 + 2 * n2, D, generator=torch.Generator().manual_seed(9)).bfloat16()
+    xd = x.to(DEV)
+    free = torch.arange(nblk - 1, nblk - 41, -1, dtype=torch.int32, device=DEV)
+    table = torch.zeros(B, 8, dtype=torch.int32, device=DEV)
+    slots, kv, cu, _ = fia.fia_block_table_append(i32([0] * B), i32(lens), free, table, block_size=bs, num_tokens=T)
+    assert int(slots.max()) >= (nblk - 1) * bs and int(table.max()) == nblk - 1
+    k, v = xd[:, n1:n1 + n2], xd[:, n1 + n2:]
+    fia.fia_cache_write(k, v, kc, vc, slots)
+    f = f64(x)
+    at, rows, ends = 0, [], []
+    for n in lens:
+        rows.append((f[at:at + n, n1:n1 + n2], f[at:at + n, n1 + n2:]))
+        at += n
+        ends.append(at - 1)
+    kw = dict(block_table=table, block_size=bs, actual_seq_kvlen=kv, num_heads=n1, num_key_value_heads=n2, scale_value=0.09,
+              softmax_lse_flag=True)
+    q = xd[ends][:, :n1].reshape(B, n1, 1, D).contiguous()
+    out, lse = fia.fia_decode_window(q, kc, vc, input_layout="BNSD", pre_tokens=200, sink_tokens=3, **kw)
+    po.assert_close(out, lse, po.decode(q.cpu(), rows, lens, 200, 3, 0.09), "decode")
+    out, lse = fia.fia_prefill_window(xd[:, :n1].contiguous(), kc, vc, input_layout="TND", actual_seq_qlen=cu, pre_tokens=200,
+                                      sink_tokens=3, **kw)
+    at = 0
+    for b, n in enumerate(lens):
+        ref = po.attend(f[at:at + n, :n1], *rows[b], po.window_see(n, n, 200, 3), 0.09)
+        po.assert_close(out[at:at + n], lse[at:at + n, :, 0], ref, f"prefill {b}")
+        at += n
+    # the last sequence's first block as everybody's prefix
+    shared = table.clone()
+    shared[:, 0] = table[2, 0]
+    kw["block_table"] = shared
+    rows = [tuple(np.concatenate([rows[2][i][:bs], r[i][bs:]]) for i in (0, 1)) for r in rows]
+    out, lse = fia.fia_decode_shared_prefix(q, kc, vc, input_layout="BNSD", shared_prefix_len=bs, **kw)
+    po.assert_close(out, lse, po.decode(q.cpu(), rows, lens, 1 << 40, 0, 0.09), "prefix")
+
+
+def test_no_keys_at_all(fia):
+    """Contiguous keys of no rows, an empty pool, lengths of zero: zeros and +inf."""
+    q = torch.randn(2, 4, 1, 64, device=DEV).bfloat16()
+    k = torch.zeros(2, 2, 0, 64, dtype=torch.bfloat16, device=DEV)
+    kw = dict(num_heads=4, num_key_value_heads=2, input_layout="BNSD", softmax_lse_flag=True)
+    pool = torch.zeros(0, 2, 16, 64, dtype=torch.bfloat16, device=DEV)
+    paged = dict(block_table=torch.zeros(2, 3, dtype=torch.int32, device=DEV), block_size=16, **kw)
+    for out, lse in (fia.fia_decode_window(q, k, k, **kw), fia.fia_decode_window(q, pool, pool, actual_seq_kvlen=i32([20, 0]), **paged),
+                     fia.fia_decode_shared_prefix(q, pool, pool, shared_prefix_len=16, actual_seq_kvlen=i32([20, 40]), **paged)):
+        if lse is not None:
+            assert torch.isfinite(out).all()
+    out, lse = fia.fia_decode_window(q, k, k, **kw)
+    assert (out == 0).all() and torch.isposinf(lse).all()
