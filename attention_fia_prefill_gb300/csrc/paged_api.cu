@@ -2,6 +2,7 @@
 // validation and launches.  Lengths stay on the device; nothing here waits for
 // the GPU or copies to it.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -27,10 +28,21 @@ fia_status check_i32(const fia_tensor* t, int64_t n, const char* name) {
   return FIA_OK;
 }
 
-bool overlap(const fia_tensor* a, const fia_tensor* b) {   // int32 tensors
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a->data), b0 = reinterpret_cast<uintptr_t>(b->data);
-  const uintptr_t na = uintptr_t(numel(a)) * 4, nb = uintptr_t(numel(b)) * 4;
+bool overlap(const void* a, uintptr_t na, const void* b, uintptr_t nb) {   // bytes
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   return na > 0 && nb > 0 && a0 < b0 + nb && b0 < a0 + na;
+}
+bool overlap(const fia_tensor* a, const fia_tensor* b) {   // int32 tensors
+  return overlap(a->data, uintptr_t(numel(a)) * 4, b->data, uintptr_t(numel(b)) * 4);
+}
+
+// The kernels scale scores in log2 units with one fp32 factor, and a hidden
+// score is -inf: a factor that is 0 there would make it NaN.
+fia_status check_scale(const fia_params* prm) {
+  const float f = float(prm->scale_value * 1.4426950408889634);
+  if (!(f >= FLT_MIN) || !std::isfinite(f))
+    return fail(FIA_ERR_UNSUPPORTED, "scale_value must be > 0 and, times log2(e), a normal fp32 number");
+  return FIA_OK;
 }
 
 #define FIA_TRY(x)                        \
@@ -97,8 +109,7 @@ fia_status span_params(const fia_tensor* q, const fia_tensor* k, const fia_tenso
   if (D != 64 && D != 128) return fail(FIA_ERR_UNSUPPORTED, "decode head dim %lld (kernels take 64 or 128)", (long long)D);
   if (N1 / N2 * S > 64)
     return fail(FIA_ERR_UNSUPPORTED, "decode rows per KV head (Q_N / KV_N x Q_S = %lld) above 64", (long long)(N1 / N2 * S));
-  if (!(prm->scale_value > 0.0) || !std::isfinite(prm->scale_value))
-    return fail(FIA_ERR_UNSUPPORTED, "scale_value must be finite and > 0");
+  FIA_TRY(check_scale(prm));
   if (!same_shape(k, v)) return fail(FIA_ERR_SHAPE, "key and value shapes differ");
   if (!aligned16(q->data) || !aligned16(k->data) || !aligned16(v->data) || !aligned16(out->data))
     return fail(FIA_ERR_ALIGNMENT, "query/key/value/attention_out must be 16-byte aligned");
@@ -193,8 +204,7 @@ fia_status window_prefill(const fia_tensor* q, const fia_tensor* k, const fia_te
   if (!same_shape(k, v)) return fail(FIA_ERR_SHAPE, "key and value shapes differ");
   FIA_TRY(dense_dims(q, L, w.N1, w.B, w.S1, w.D, "query"));
   if (w.D != 64 && w.D != 128) return fail(FIA_ERR_UNSUPPORTED, "head dim %lld (kernels take 64 or 128)", (long long)w.D);
-  if (!(prm->scale_value > 0.0) || !std::isfinite(prm->scale_value))
-    return fail(FIA_ERR_UNSUPPORTED, "scale_value must be finite and > 0");
+  FIA_TRY(check_scale(prm));
   if (prm->pre_tokens < 0) return fail(FIA_ERR_UNSUPPORTED, "pre_tokens must be 0 or more");
   if (sink < 0) return fail(FIA_ERR_UNSUPPORTED, "sink_tokens must be 0 or more");
   if (!aligned16(q->data) || !aligned16(k->data) || !aligned16(v->data) || !aligned16(out->data))
@@ -383,6 +393,15 @@ fia_status fia_cache_write(const fia_tensor* key, int64_t key_token_stride, cons
   FIA_TRY(write_side(key, key_token_stride, key_cache, T, nblk, bs, 0, p, "key"));
   if (two) FIA_TRY(write_side(value, value_token_stride, value_cache, T, nblk, bs, 1, p, "value"));
   if (T == 0 || nblk == 0) return FIA_OK;
+  // (a row read while another token's is written over it would be a mixture)
+  for (int y = 0; y < (two ? 2 : 1); ++y) {
+    const uintptr_t pool = uintptr_t(nblk) * uintptr_t(p.dst_blk[y]);
+    for (int x = 0; x < (two ? 2 : 1); ++x)
+      if (overlap(p.src[x], uintptr_t(T - 1) * uintptr_t(p.src_row[x]) + uintptr_t(p.vecs[x]) * 16, p.dst[y], pool))
+        return fail(FIA_ERR_UNSUPPORTED, "key or value overlaps a cache");
+    if (y == 1 && overlap(p.dst[0], uintptr_t(nblk) * uintptr_t(p.dst_blk[0]), p.dst[1], pool))
+      return fail(FIA_ERR_UNSUPPORTED, "key_cache and value_cache overlap");
+  }
   p.slots = static_cast<const int32_t*>(slot_mapping->data);
   p.n_slots = nblk > kMaxInt / bs ? kMaxInt : nblk * bs;
   p.n_tokens = int(T);

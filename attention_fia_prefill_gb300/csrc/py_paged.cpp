@@ -232,7 +232,10 @@ int64_t token_stride(const at::Tensor& t, const char* name) {
   const int64_t N = t.size(1), D = t.size(2);
   if ((D > 1 && t.stride(2) != 1) || (N > 1 && t.stride(1) != D))
     raise(PyExc_ValueError, std::string(name) + ": the heads and columns of a token must be contiguous");
-  return t.size(0) > 1 ? t.stride(0) : N * D;
+  if (t.size(0) < 2) return N * D;
+  // (the C entry reads a stride of 0 as "contiguous")
+  if (t.stride(0) < N * D) raise(PyExc_ValueError, std::string(name) + ": tokens must not share memory");
+  return t.stride(0);
 }
 
 // key, value, key_cache, value_cache, slot_mapping

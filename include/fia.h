@@ -364,7 +364,8 @@ FIA_API fia_status fia_block_table_append(const fia_tensor* context_lens, const 
  *          multiple of 16.  value and value_cache may both be NULL.
  *   key_cache / value_cache: (blocknum, KV_N, block_size, D) or (blocknum,
  *          block_size, KV_N*D), the same blocknum and block_size, the
- *          tensors' types.
+ *          tensors' types.  The caches may overlap neither each other nor key
+ *          or value.
  *   slot_mapping: int32 (T): token t goes to row slot % block_size of block
  *          slot / block_size.  Slots outside the pool (negative ones among
  *          them) are skipped; every other row of the pools stays as it was.
@@ -389,8 +390,11 @@ FIA_API fia_status fia_cache_write(const fia_tensor* key, int64_t key_token_stri
  *          clamped to [0, keys the tensors have room for]; NULL: all of them
  *          (contiguous key/value only).  params' own lists must be NULL.
  *   params->pre_tokens >= 0 (default 2^31-1: no window), sink_tokens >= 0.
- *          sparse_mode and next_tokens are not read.
- *   Rows that see no key (p < 0: a padded batch) give 0 and +inf.
+ *          sparse_mode and next_tokens are not read.  scale_value * log2(e) must
+ *          be a normal fp32 number (also of the two entries below).
+ *   Rows that see no key (p < 0: a padded batch) give 0 and +inf.  With several
+ *          new tokens the values (not scores) of a key that only some of them
+ *          see enter the others' sums with a weight of 0: they must be finite.
  *   No workspace.
  * ------------------------------------------------------------------------ */
 FIA_API fia_status fia_decode_window(const fia_tensor* query, const fia_tensor* key, const fia_tensor* value,

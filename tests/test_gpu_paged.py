@@ -507,3 +507,13 @@ def test_binding_checks(fia):
     with pytest.raises(fia.FIAError, match="overlap"):
         fia.fia_block_table_append(z, z.clone(), z.clone(), torch.zeros(2, 2, dtype=torch.int32, device=DEV), block_size=4,
                                    num_tokens=5, kv_lens=z)
+
+
+def test_cache_write_refuses_repeated_tokens(fia):
+    """A broadcast token has a stride of 0, which the C entry reads as "contiguous"."""
+    pool = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16, device=DEV)
+    one = torch.ones(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="share memory"):
+        fia.fia_cache_write(one.expand(4, 2, 64), None, pool, None, i32([0, 1, 2, 3]))
+    fia.fia_cache_write(one.expand(1, 2, 64), None, pool, None, i32([3]))
+    assert pool[0, :, 3].eq(1).all() and pool.sum() == 128

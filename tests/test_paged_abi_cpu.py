@@ -86,6 +86,18 @@ def test_write_without_tokens_or_blocks(lib):
     assert write(lib, nb=0, kc=t((0, 2, 16, 64), BF16, None), vc=t((0, 2, 16, 64), BF16, None)) == "FIA_OK"
 
 
+@pytest.mark.parametrize("kw,names", [
+    (dict(k=t((10, 2, 64), BF16, P)), "key or value"),                                   # key inside key_cache
+    (dict(v=t((10, 2, 64), BF16, P + 5 * 2 * 16 * 64 * 2 - 16)), "key or value"),        # its last 16 bytes
+    (dict(k=t((10, 2, 64), BF16, P - 9 * 1024 - 240), ks=512), "key or value"),          # a strided key's last row
+    (dict(vc=t((5, 2, 16, 64), BF16, P + 4096)), "key_cache and value_cache"),
+])
+def test_write_refuses_overlaps(lib, kw, names):
+    far = dict(k=t((10, 2, 64), BF16, P + (1 << 20)), v=t((10, 2, 64), BF16, P + (2 << 20)), vc=t((5, 2, 16, 64), BF16, P + (3 << 20)))
+    assert write(lib, **{**far, **kw}) == "FIA_ERR_UNSUPPORTED"
+    assert names in lib.fia_last_error().decode()
+
+
 # ------------------------------------------------------------------ windowed decode
 def window(lib, B_=2, n1=8, n2=2, Q=1, D=128, nb=9, bs=32, sink=4, prm=None, **kw):
     p = dict(num_heads=n1, num_key_value_heads=n2, input_layout="BNSD", block_size=bs, pre_tokens=100)
@@ -277,3 +289,11 @@ def test_prefix_workspace(lib):
     for ws, have, want in ((None, n, "FIA_ERR_WORKSPACE"), (P, 256, "FIA_ERR_WORKSPACE"), (P + 8, n, "FIA_ERR_ALIGNMENT")):
         assert code(lib.fia_decode_shared_prefix(q, k, k, t((4, 8), I32), t((4,), I32), ctypes.byref(prm.p), 512, q, None, ws,
                                                  have, None)) == want
+
+
+@pytest.mark.parametrize("scale", [1e-60, 1e-39, 1e300, float("inf")])
+def test_scale_has_to_fit_fp32(lib, scale):
+    """A factor that is 0 (or infinite) in fp32 times a hidden score of -inf is a NaN."""
+    assert window(lib, prm=dict(scale_value=scale)) == "FIA_ERR_UNSUPPORTED"
+    assert prefill(lib, prm=dict(scale_value=scale)) == ("FIA_ERR_UNSUPPORTED",) * 2
+    assert prefix(lib, prm=dict(scale_value=scale)) == ("FIA_ERR_UNSUPPORTED",) * 2
