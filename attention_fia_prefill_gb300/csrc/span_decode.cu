@@ -30,6 +30,11 @@
 //     launch, no workspace, no atomics, the same bits on every run.  Each CTA
 //     sends its results to the CTA that writes them (one barrier; reading them
 //     there took a second one, so that no CTA left while it was read: 1.5 us).
+// Bound: HBM where spans are long (64 sequences x 4 tokens, window 4096: 165 us,
+// 94% of a copy's rate); where they are short the chain length -> page ids ->
+// keys -> join and code fetched for one use (16 sequences, window 1024: 14.5 us,
+// 59%; one sequence 6.3 us); units of 32 and 64 rows are bound by mma.sync and
+// the fragments' loads (57% and 35%).
 #include <algorithm>
 #include <type_traits>
 
