@@ -38,15 +38,13 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "paged.h"
-#include "ptx.cuh"
+#include "span_join.cuh"
 
 namespace fia {
 namespace {
 
 constexpr int kSpanThreads = 128;
 constexpr int kSpanTile = 16;        // keys of a tile
-constexpr int kMostCtas = 8;         // CTAs of a unit (a portable cluster)
 
 template <int D, int MT>
 struct SpanCfg {
@@ -63,12 +61,10 @@ struct SpanCfg {
   // after the loop the rings hold O of every group [kGroups][16 MT][D]
   static constexpr int kO = kGroups * 16 * MT * D * 4;
   static_assert(kO <= kRing, "the groups' results take the rings' place");
-  // (max, sum) of every group; results of the cluster's CTAs for this CTA's
-  // share of the unit's float4s, and their (max, sum) of every row
+  // (max, sum) of every group; what the join receives
   static constexpr int kOffML = kRing;
   static constexpr int kOffIn = kOffML + kGroups * 16 * MT * 8;
-  static constexpr int kOffInML = kOffIn + (16 * MT * (D / 4) + 8 * kMostCtas) * 16;
-  static constexpr int kSmem = kOffInML + kMostCtas * 16 * MT * 8 + 128;
+  static constexpr int kSmem = kOffIn + JoinIn<D, 16 * MT>::kBytes + 128;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -101,27 +97,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// The cluster's barrier in halves: arrive releases this thread's writes, wait
-// acquires every CTA's.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t peer_addr(uint32_t smem, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ void st_peer4(uint32_t a, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void st_peer2(uint32_t a, float2 v) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
-}
-
-// The weight of a partial result with maximum m in a sum with maximum top
-// (an empty one, m = -inf, has none).
-__device__ __forceinline__ float join_weight(float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); }
-
 template <int D, bool BF16, int MT>
 __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_decode_kernel(const __grid_constant__ SpanParams p) {
   using C = SpanCfg<D, MT>;
@@ -140,7 +115,6 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   // instruction cache: a division is twenty instructions, at ten cycles each.
   const uint32_t lg = uint32_t(p.lg_cs), cs = 1u << lg, rank = blockIdx.x & (cs - 1u);
   const int b = int(blockIdx.x >> lg), kvh = blockIdx.y;
-  auto head_of = [&](int r) -> int { return int((uint32_t(r) * p.q_inv) >> 16); };   // r / q_tokens, r < 64
 
   grid_dep_launch();
   if (lg != 0) cluster_arrive();   // (waited for before the join's first remote store: every CTA runs by then)
@@ -175,7 +149,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   // columns 2 ft, 2 ft + 1 and 8 + 2 ft, 9 + 2 ft of every 16
   const int r0 = rt * 16 + fg, r1 = r0 + 8;
   const T* qp = static_cast<const T*>(p.q) + int64_t(b) * p.q_sb + 2 * ft;
-  const int h0 = head_of(r0), h1 = head_of(r1), tk0 = r0 - h0 * p.q_tokens, tk1 = r1 - h1 * p.q_tokens;
+  const int h0 = span_head(p, r0), h1 = span_head(p, r1), tk0 = r0 - h0 * p.q_tokens, tk1 = r1 - h1 * p.q_tokens;
   const T* q0 = qp + (kvh * p.group + h0) * p.q_sn + tk0 * p.q_ss;
   const T* q1 = qp + (kvh * p.group + h1) * p.q_sn + tk1 * p.q_ss;
   uint32_t qa[KK][4];
@@ -369,153 +343,28 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
 
   // ---------------------------------------------------------------- join
-  // [group][16 MT rows][D] with the float4s of a row XOR-swizzled by row, so
-  // that the rows of a store instruction do not share banks
   __syncthreads();           // every ring has been read
   float* ob = reinterpret_cast<float*>(smem);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffML);
-  auto at = [&](int g, int r, int c4) -> int { return ((g * 16 * MT + r) * (D / 4) + (c4 ^ ((r & 7) << 1))) * 4; };
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int c = t * 8 + 2 * ft;
-    *reinterpret_cast<float2*>(ob + at(kg, r0, c >> 2) + (c & 3)) = make_float2(o[t][0], o[t][1]);
-    *reinterpret_cast<float2*>(ob + at(kg, r1, c >> 2) + (c & 3)) = make_float2(o[t][2], o[t][3]);
+    *reinterpret_cast<float2*>(ob + join_at<D, 16 * MT>(kg, r0, c >> 2) + (c & 3)) = make_float2(o[t][0], o[t][1]);
+    *reinterpret_cast<float2*>(ob + join_at<D, 16 * MT>(kg, r1, c >> 2) + (c & 3)) = make_float2(o[t][2], o[t][3]);
   }
   if (ft == 0) {
     ml[kg * 16 * MT + r0] = make_float2(m0, l0);
     ml[kg * 16 * MT + r1] = make_float2(m1, l1);
   }
-  __syncthreads();
-  // This CTA's groups joined, float4 by float4, each sent to the CTA that
-  // writes it: the CTAs of the cluster take eight in turn.
-  const int items = p.rows * (D / 4);
-  const int share = ((items + 8 * int(cs) - 1) >> (3 + lg)) << 3;
-  const uint32_t in_o = smem_u32(smem + C::kOffIn), in_ml = smem_u32(smem + C::kOffInML);
-  __syncwarp();
-  if (lg != 0) cluster_wait();
-  for (int e = threadIdx.x; e < items; e += kSpanThreads) {
-    const int r = e / (D / 4), c4 = e % (D / 4);
-    float top = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < C::kGroups; ++g) top = fmaxf(top, ml[g * 16 * MT + r].x);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll
-    for (int g = 0; g < C::kGroups; ++g) {
-      const float2 w2 = ml[g * 16 * MT + r];
-      const float w = join_weight(w2.x, top);
-      const float4 x = *reinterpret_cast<const float4*>(ob + at(g, r, c4));
-      l += w * w2.y;
-      a.x += w * x.x; a.y += w * x.y; a.z += w * x.z; a.w += w * x.w;
-    }
-    const int owner = (e >> 3) & int(cs - 1u), slot = ((e >> (3 + lg)) << 3) + (e & 7);
-    st_peer4(peer_addr(in_o + (rank * share + slot) * 16, owner), a);
-    if (c4 == 0)
-      for (uint32_t k = 0; k < cs; ++k) st_peer2(peer_addr(in_ml + (rank * 16 * MT + r) * 8, k), make_float2(top, l));
-  }
-  __syncwarp();
-  if (lg != 0) cluster_arrive();
-  if (p.n_parts > 0) grid_dep_wait();   // (by every thread: the prefix's results are in)
-  if (lg != 0) cluster_wait(); else __syncthreads();   // no CTA reads or writes another's memory from here on
-  const float4* xo = reinterpret_cast<const float4*>(smem + C::kOffIn);
-  const float2* xml = reinterpret_cast<const float2*>(smem + C::kOffInML);
-  for (int i = threadIdx.x; i < share; i += kSpanThreads) {
-    const int e = ((((i >> 3) << lg) + int(rank)) << 3) + (i & 7);
-    if (e >= items) break;
-    const int r = e / (D / 4), c4 = e % (D / 4);
-    const int h = head_of(r), head = kvh * p.group + h, tokn = r - h * p.q_tokens;
-    float top = -INFINITY;
-    for (uint32_t g = 0; g < cs; ++g) top = fmaxf(top, xml[g * 16 * MT + r].x);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (uint32_t g = 0; g < cs; ++g) {
-      const float2 w2 = xml[g * 16 * MT + r];
-      const float w = join_weight(w2.x, top);
-      const float4 x = xo[g * share + i];
-      l += w * w2.y;
-      a.x += w * x.x; a.y += w * x.y; a.z += w * x.z; a.w += w * x.w;
-    }
-    // the prefix's parts, kBatch loads in flight, with a running maximum
-    constexpr int kBatch = D == 64 ? 16 : 24;
-    const int64_t prow = (int64_t(b) * p.N1 + head) * p.q_tokens + tokn;
-    for (int g0 = 0; g0 < p.n_parts; g0 += kBatch) {
-      float2 w2[kBatch];
-      float4 x[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const bool in = g0 + k < p.n_parts;
-        const int64_t row = (in ? g0 + k : g0) * p.part_rows + prow;
-        w2[k] = p.part_ml[row];
-        x[k] = *reinterpret_cast<const float4*>(p.part_o + row * D + c4 * 4);
-        if (!in) w2[k].x = -INFINITY;
-      }
-      float t = top;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) t = fmaxf(t, w2[k].x);
-      const float keep = join_weight(top, t);
-      l *= keep;
-      a.x *= keep; a.y *= keep; a.z *= keep; a.w *= keep;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (w2[k].x == -INFINITY) continue;   // an empty part: its O may be 0 * NaN
-        const float w = join_weight(w2[k].x, t);
-        l += w * w2[k].y;
-        a.x += w * x[k].x; a.y += w * x[k].y; a.z += w * x[k].z; a.w += w * x[k].w;
-      }
-      top = t;
-    }
-    const bool has = l != 0.f;   // a NaN sum stays a NaN
-    const float inv = has ? 1.f / l : 0.f;
-    uint2 u;
-    u.x = has ? pack2(a.x * inv, a.y * inv, BF16) : 0u;
-    u.y = has ? pack2(a.z * inv, a.w * inv, BF16) : 0u;
-    T* orow = static_cast<T*>(p.out) + int64_t(b) * p.q_sb + int64_t(head) * p.q_sn + int64_t(tokn) * p.q_ss;
-    *reinterpret_cast<uint2*>(orow + c4 * 4) = u;
-    if (p.lse != nullptr && c4 == 0)
-      p.lse[int64_t(b) * p.lse_sb + int64_t(head) * p.lse_sn + int64_t(tokn) * p.lse_ss] =
-          has ? (top + __log2f(l)) * 0.69314718055994531f : INFINITY;
-  }
+  span_join<D, BF16, 16 * MT, C::kGroups, kSpanThreads>(p, ob, ml, smem + C::kOffIn, lg, rank, b, kvh);
 }
 
 template <int D, bool BF16, int MT>
-cudaError_t launch_one(const SpanParams& p, int cs, cudaStream_t s) {
+cudaError_t launch_one(const SpanParams& p, cudaStream_t s) {
   using C = SpanCfg<D, MT>;
   cudaError_t e = set_smem_once<span_decode_kernel<D, BF16, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.B * cs), unsigned(p.N2));
-  cfg.blockDim = dim3(kSpanThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(cs);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, span_decode_kernel<D, BF16, MT>, p);
-}
-
-// CTAs of a unit: those whose waves take the least time, a CTA costing its
-// groups' tiles and about kSpanStart more (launch, length, page ids, first
-// keys, join).  Where the keys' limit is not the window's but the tables'
-// the lengths behind it vary, and smaller shares even them out: up to a
-// seventh more by this count is taken for them.  (Sweep over 1, 2, 4, 8 CTAs,
-// us: 16 sequences x 8 heads, window of 65 tiles 24.0, 17.8, 25.6, 41.1; 64 x 8,
-// 257 tiles 170, 193, 197, 273; 32 x 8, lengths up to 513 tiles 133, 113, 106, 128.)
-constexpr int kSpanStart = 4;
-int cluster_ctas(int64_t units, int64_t tiles, int groups, bool even, int64_t slots) {
-  int best = 1;
-  int64_t least = 0;
-  for (int cs = 1; cs <= kMostCtas; cs *= 2) {
-    const int64_t waves = (units * cs + slots - 1) / slots;
-    const int64_t cost = waves * ((tiles + cs * groups - 1) / (cs * groups) + kSpanStart);
-    if (cs == 1 || (even ? cost < least : cost * 7 < least * 8)) best = cs;
-    if (cs == 1 || cost < least) least = cost;
-  }
-  return best;
+  return launch_span(span_decode_kernel<D, BF16, MT>, p, p, kSpanThreads, C::kSmem, s);
 }
 
 }  // namespace
@@ -524,18 +373,13 @@ cudaError_t launch_span_decode(const SpanParams& params, int head_dim, bool bf16
   SpanParams p = params;
   const int mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
   const int64_t span = std::min<int64_t>(p.kv_max - p.base, int64_t(p.sink) + p.pre + p.q_tokens);
-  const int cs = cluster_ctas(int64_t(p.B) * p.N2, span / kSpanTile + 1, 4 / mt,
-                              span < p.kv_max - p.base, (head_dim == 64 ? 4 : 2) * n_sm);
-  p.lg_cs = cs == 8 ? 3 : cs / 2;
-  p.q_inv = 65536u / unsigned(p.q_tokens) + 1u;   // floor(r q_inv / 2^16) = r / q_tokens for r < 64, q_tokens <= 16
-  p.lg_block = -1;
-  for (int k = 4; k < 31; ++k)
-    if (p.block_size == 1 << k) p.lg_block = k;
+  set_span_shape(p, cluster_ctas(int64_t(p.B) * p.N2, span / kSpanTile + 1, 4 / mt, span < p.kv_max - p.base,
+                                 (head_dim == 64 ? 4 : 2) * n_sm));
 #define FIA_SPAN(DD, BB)                                    \
   switch (mt) {                                             \
-    case 1: return launch_one<DD, BB, 1>(p, cs, s);         \
-    case 2: return launch_one<DD, BB, 2>(p, cs, s);         \
-    default: return launch_one<DD, BB, 4>(p, cs, s);        \
+    case 1: return launch_one<DD, BB, 1>(p, s);             \
+    case 2: return launch_one<DD, BB, 2>(p, s);             \
+    default: return launch_one<DD, BB, 4>(p, s);        \
   }
   if (head_dim == 128) {
     if (bf16) { FIA_SPAN(128, true) } else { FIA_SPAN(128, false) }
