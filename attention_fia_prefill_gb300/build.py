@@ -23,7 +23,7 @@ LIB = os.path.join(OUT_DIR, "libfia.so")
 EXT = os.path.join(OUT_DIR, "_fia_paged.so")
 EXT_SOURCE = os.path.join(CSRC, "py_paged.cpp")
 SOURCES = ["fia_api.cu", "prefill.cu", "prefill_pair.cu", "bsa_fp8.cu", "decode.cu", "decode_d64.cu", "decode_gqa.cu", "decode_noalloc.cu",
-           "mla.cu", "paged_api.cu", "paged.cu", "span_decode.cu", "prefill_window.cu"]
+           "mla.cu", "paged_api.cu", "paged.cu", "span_decode.cu", "span_wide.cu", "prefill_window.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fvisibility=hidden", "-cudart", "shared"]

@@ -5,6 +5,7 @@
 #pragma once
 #include <cstdint>
 
+#include "../../include/fia.h"
 #include "internal.h"
 
 namespace fia {
@@ -73,5 +74,9 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t s);
 // on the device).
 cudaError_t launch_prefill_window(const PrefillParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s);
 cudaError_t launch_span_decode(const SpanParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s);
+// The same for units of 17..64 rows, on the tcgen05 tensor cores (fia_status: it
+// builds tensor maps), and whether it is the faster one.
+bool span_wide_pays(const SpanParams& p, int n_sm);
+fia_status launch_span_wide(const SpanParams& p, int head_dim, bool bf16, int n_sm, cudaStream_t s);
 
 }  // namespace fia

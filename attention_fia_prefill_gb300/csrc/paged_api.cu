@@ -178,6 +178,22 @@ fia_status span_params(const fia_tensor* q, const fia_tensor* k, const fia_tenso
   return FIA_OK;
 }
 
+// Launches the decode over a visible span.
+fia_status run_span(const SpanParams& p, int64_t D, bool bf16, int n_sm, cudaStream_t s) {
+  if (span_wide_pays(p, n_sm)) return launch_span_wide(p, int(D), bf16, n_sm, s);
+  return cuda_check(launch_span_decode(p, int(D), bf16, n_sm, s), "decode launch");
+}
+
+// ... as the call's main kernel (the caller's events around it).
+fia_status run_profiled(const SpanParams& p, int64_t D, bool bf16, int n_sm, cudaStream_t s) {
+  fia_status st = FIA_OK;
+  const cudaError_t e = profiled(s, [&] {
+    st = run_span(p, D, bf16, n_sm, s);
+    return cudaSuccess;
+  });
+  return st != FIA_OK ? st : cuda_check(e, "profiling events");
+}
+
 // Arguments of fia_prefill_window -> launch parameters without the tensor maps.
 struct WindowPrefill {
   PrefillParams p;
@@ -422,9 +438,7 @@ fia_status fia_decode_window(const fia_tensor* query, const fia_tensor* key, con
   if (sink_tokens < 0) return fail(FIA_ERR_UNSUPPORTED, "sink_tokens must be 0 or more");
   p.sink = int(std::min<int64_t>(sink_tokens, p.kv_max));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_check(
-      profiled(s, [&] { return launch_span_decode(p, int(D), query->dtype == FIA_DTYPE_BF16, sm_count(), s); }),
-      "window decode launch");
+  return run_profiled(p, D, query->dtype == FIA_DTYPE_BF16, sm_count(), s);
 }
 
 fia_status fia_prefill_window_get_workspace_size(const fia_tensor* query, const fia_tensor* key,
@@ -519,7 +533,7 @@ fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* k
   uint8_t* base = static_cast<uint8_t*>(workspace);
   if (!w.split_off) {
     FIA_TRY(cuda_check(cudaMemsetAsync(base, 0, 8, s), "status reset"));
-    return cuda_check(profiled(s, [&] { return launch_span_decode(p, int(D), bf16, n_sm, s); }), "decode launch");
+    return run_profiled(p, D, bf16, n_sm, s);
   }
   PrefillParams pp;
   memset(&pp, 0, sizeof(pp));
@@ -566,7 +580,7 @@ fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* k
   p.part_ml = pp.part_ml;
   p.n_parts = w.n_splits;
   p.part_rows = w.rows;
-  return cuda_check(launch_span_decode(p, int(D), bf16, n_sm, s), "decode launch");
+  return run_span(p, D, bf16, n_sm, s);
 }
 
 }  // extern "C"

@@ -8,13 +8,13 @@
 //
 // Lengths are read on the device, so the grid depends on sizes alone and a
 // captured call follows new lengths.  A unit is (batch, kv head), its rows the
-// g heads x Q_S tokens (at most 64).  Its keys are the 16-key tiles of the
-// sinks and of [first row's window, L): a list whose length the device knows.
+// g heads x Q_S tokens: up to 32 here, more (and 17..32 with many keys) in
+// span_wide.cu.  Its keys are the 16-key tiles of the sinks and of [first row's
+// window, L): a list whose length the device knows.
 //   * Work: a cluster of 1..8 CTAs runs a unit, each CTA four warps.  A warp
 //     owns 16 rows (mma.sync m16n8k16); units of up to 16 rows give each warp
 //     keys of its own (tile v of the list belongs to group v mod groups), those
-//     of 32 / 64 rows pair / quadruple the warps of a group over the same tiles,
-//     two / four of them a step.
+//     of 17..32 pair the warps of a group over the same tiles, two a step.
 //   * Data: a group streams its tiles through a ring of its own with cp.async
 //     (16-byte pieces, XOR-swizzled so that ldmatrix has no bank conflicts): no
 //     barrier across groups in the loop.  A tile lies in one page (16 divides
@@ -30,11 +30,10 @@
 //     launch, no workspace, no atomics, the same bits on every run.  Each CTA
 //     sends its results to the CTA that writes them (one barrier; reading them
 //     there took a second one, so that no CTA left while it was read: 1.5 us).
-// Bound: HBM where spans are long (64 sequences x 4 tokens, window 4096: 165 us,
-// 94% of a copy's rate); where they are short the chain length -> page ids ->
+// Bound: HBM where spans are long (64 sequences x 4 tokens, window 4096: 163 us,
+// 95% of a copy's rate); where they are short the chain length -> page ids ->
 // keys -> join and code fetched for one use (16 sequences, window 1024: 14.5 us,
-// 59%; one sequence 6.3 us); units of 32 and 64 rows are bound by mma.sync and
-// the fragments' loads (57% and 35%).
+// 59%; one sequence 6.3 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -369,22 +368,27 @@ cudaError_t launch_one(const SpanParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// Start cost of a CTA in its groups' 16-key tiles.  (Sweep over 1, 2, 4, 8
+// CTAs of a unit, us: 16 sequences x 8 heads, window of 65 tiles 24.0, 17.8, 25.6,
+// 41.1; 64 x 8, 257 tiles 170, 193, 197, 273; 32 x 8, lengths up to 513 tiles
+// 133, 113, 106, 128.  Where the keys' limit is the tables' and not the window's
+// the lengths behind it vary.)
+constexpr int kSpanStart = 4;
+
 cudaError_t launch_span_decode(const SpanParams& params, int head_dim, bool bf16, int n_sm, cudaStream_t s) {
   SpanParams p = params;
-  const int mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+  if (p.rows > 32) return cudaErrorInvalidValue;
+  const int mt = p.rows <= 16 ? 1 : 2;
   const int64_t span = std::min<int64_t>(p.kv_max - p.base, int64_t(p.sink) + p.pre + p.q_tokens);
-  set_span_shape(p, cluster_ctas(int64_t(p.B) * p.N2, span / kSpanTile + 1, 4 / mt, span < p.kv_max - p.base,
-                                 (head_dim == 64 ? 4 : 2) * n_sm));
-#define FIA_SPAN(DD, BB)                                    \
-  switch (mt) {                                             \
-    case 1: return launch_one<DD, BB, 1>(p, s);             \
-    case 2: return launch_one<DD, BB, 2>(p, s);             \
-    default: return launch_one<DD, BB, 4>(p, s);        \
-  }
+  set_span_shape(p, cluster_ctas(int64_t(p.B) * p.N2, span / kSpanTile + 1, 4 / mt, kSpanStart,
+                                 span < p.kv_max - p.base, (head_dim == 64 ? 4 : 2) * n_sm));
+#define FIA_SPAN(DD, BB) return mt == 1 ? launch_one<DD, BB, 1>(p, s) : launch_one<DD, BB, 2>(p, s)
   if (head_dim == 128) {
-    if (bf16) { FIA_SPAN(128, true) } else { FIA_SPAN(128, false) }
+    if (bf16) FIA_SPAN(128, true);
+    FIA_SPAN(128, false);
   }
-  if (bf16) { FIA_SPAN(64, true) } else { FIA_SPAN(64, false) }
+  if (bf16) FIA_SPAN(64, true);
+  FIA_SPAN(64, false);
 #undef FIA_SPAN
 }
 

@@ -1,4 +1,4 @@
-// The end of a span decode unit (span_decode.cu): the results of
+// The end of a span decode unit (span_decode.cu, span_wide.cu): the results of
 // a CTA's groups, of the unit's CTAs and of a shared prefix, joined and written.
 #pragma once
 #include <algorithm>
@@ -166,19 +166,15 @@ __device__ __forceinline__ void span_join(const SpanParams& p, const float* ob, 
 
 // ------------------------------------------------------------------- host
 // CTAs of a unit: those whose waves take the least time, a CTA costing its
-// groups' tiles and about kSpanStart more (launch, length, page ids, first
-// keys, join).  Where the keys' limit is not the window's but the tables'
-// the lengths behind it vary, and smaller shares even them out: up to a
-// seventh more by this count is taken for them.  (Sweep over 1, 2, 4, 8 CTAs,
-// us: 16 sequences x 8 heads, window of 65 tiles 24.0, 17.8, 25.6, 41.1; 64 x 8,
-// 257 tiles 170, 193, 197, 273; 32 x 8, lengths up to 513 tiles 133, 113, 106, 128.)
-constexpr int kSpanStart = 4;
-inline int cluster_ctas(int64_t units, int64_t tiles, int groups, bool even, int64_t slots) {
+// groups' tiles and about `start` tiles more (launch, length, page ids, first
+// keys, join).  even: units have like lengths; else smaller shares even them out,
+// and up to a seventh more by this count is taken for them.
+inline int cluster_ctas(int64_t units, int64_t tiles, int groups, int start, bool even, int64_t slots) {
   int best = 1;
   int64_t least = 0;
   for (int cs = 1; cs <= kMostCtas; cs *= 2) {
     const int64_t waves = (units * cs + slots - 1) / slots;
-    const int64_t cost = waves * ((tiles + cs * groups - 1) / (cs * groups) + kSpanStart);
+    const int64_t cost = waves * ((tiles + cs * groups - 1) / (cs * groups) + start);
     if (cs == 1 || (even ? cost < least : cost * 7 < least * 8)) best = cs;
     if (cs == 1 || cost < least) least = cost;
   }

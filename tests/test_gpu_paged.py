@@ -517,3 +517,84 @@ def test_cache_write_refuses_repeated_tokens(fia):
         fia.fia_cache_write(one.expand(4, 2, 64), None, pool, None, i32([0, 1, 2, 3]))
     fia.fia_cache_write(one.expand(1, 2, 64), None, pool, None, i32([3]))
     assert pool[0, :, 3].eq(1).all() and pool.sum() == 128
+
+
+# ------------------------------------------------------------------ units of 17..64 rows
+@pytest.mark.parametrize("pre,sink", [(0, 0), (0, 70), (15, 4), (64, 64), (100, 0), (127, 130), (1000, 3), (BIG, 0), (40, BIG)])
+def test_wide_masks(fia, pre, sink):
+    _window(fia, [1, 2, 63, 64, 65, 300, 0, 513, 1999], 40, 1, 128, pre, sink, workload=130)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 48, 64, 96, 256])
+@pytest.mark.parametrize("kv", ["BNBD", "BSH"])
+def test_wide_pages(fia, bs, kv):
+    """Pages below a 64-key tile, that do not divide it, and above it; a window that starts inside a page."""
+    _window(fia, [1, 8, 40, 333, 777], 16, 2, 128, 99, 70, Q=8, bs=bs, kv=kv, workload=131)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("n1,n2,Q,lens,pre", [
+    (32, 1, 1, [3000, 2049, 7, 0], 2500), (24, 1, 1, [2600, 64, 2047], BIG), (18, 2, 2, [2400, 2, 1], 2100),   # 32 rows, many keys
+    (6, 2, 4, [1 + (i * 29) % 300 for i in range(90)], 270),                                                   # 180 units of 24 rows
+    (64, 1, 1, [2900], BIG), (8, 1, 8, [900, 1, 64, 65, 128], 300), (44, 4, 5, [128] * 3, BIG)])               # 33..64 rows
+def test_wide_units(fia, dt, D, n1, n2, Q, lens, pre):
+    """Both layouts of the rows in TMEM, one to eight CTAs of a unit, CTAs without a tile."""
+    _window(fia, lens, n1, n2, D, pre, 5, Q=Q, bs=64, dt=dt, workload=132 + n1)
+
+
+@pytest.mark.parametrize("layout", ["BNSD", "BSND", "BSH"])
+def test_wide_contiguous(fia, layout):
+    """A cache whose last tile ends inside the tensor; NaN rows past a length; no keys at all."""
+    B, n1, n2, S, D, Q = 2, 24, 2, 333, 64, 4
+    q = fia_inputs.normal((B, n1, Q, D), "bf16", 133, 1)
+    k, v = (fia_inputs.normal((B, n2, S, D), "bf16", 133, i) for i in (2, 3))
+    lens, scale = [333, 70], D ** -0.5
+    rows = [tuple(f64(x[b].transpose(0, 1)) for x in (k, v)) for b in range(B)]
+    k[1, :, 70:] = float("nan")
+    v[1, :, 70:] = float("nan")
+    lay = {"BNSD": lambda x: x, "BSND": lambda x: x.transpose(1, 2).contiguous(),
+           "BSH": lambda x: x.transpose(1, 2).flatten(2).contiguous()}[layout]
+    kw = dict(num_heads=n1, num_key_value_heads=n2, scale_value=scale, input_layout=layout, softmax_lse_flag=True)
+    out, lse = fia.fia_decode_window(lay(q).to(DEV), lay(k).to(DEV), lay(v).to(DEV), actual_seq_kvlen=i32(lens), pre_tokens=100,
+                                     sink_tokens=3, **kw)
+    out = out if layout == "BNSD" else out.reshape(B, Q, n1, D).transpose(1, 2)
+    po.assert_close(out, lse, po.decode(q, [(a[:n], b[:n]) for (a, b), n in zip(rows, lens)], lens, 100, 3, scale))
+    none = lay(k[:, :, :0]).to(DEV)
+    out, lse = fia.fia_decode_window(lay(q).to(DEV), none, none, **kw)
+    assert (out == 0).all() and torch.isposinf(lse).all()
+
+
+def test_wide_empty_pool_reads_as_zeros(fia):
+    """No block in the pool: every key and value of a length is 0, so out = 0 and lse = log(keys seen)."""
+    q = fia_inputs.normal((2, 40, 1, 64), "bf16", 134, 1).to(DEV)
+    pool = torch.zeros(0, 1, 32, 64, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(2, 4, dtype=torch.int32, device=DEV)
+    out, lse = fia.fia_decode_window(q, pool, pool, actual_seq_kvlen=i32([100, 0]), block_table=table, block_size=32, num_heads=40,
+                                     num_key_value_heads=1, input_layout="BNSD", softmax_lse_flag=True)
+    assert (out == 0).all() and torch.isposinf(lse[1]).all() and (lse[0] - np.log(100)).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("n1,n2,Q,B,own", [(64, 1, 1, 5, 700), (16, 2, 8, 4, 90), (48, 8, 4, 30, 300)])
+def test_wide_behind_a_prefix(fia, n1, n2, Q, B, own):
+    _prefix(fia, [Q + (i * 61) % own for i in range(B)], 512, n1, n2, 128, Q=Q, bs=128, workload=135 + n1)
+
+
+def test_wide_timeout_leaves_nan(fia):
+    """A wait that gives up leaves NaN in its unit's rows (there is no status word); the next call is right."""
+    from attention_fia_prefill_gb300 import _binding as B
+    lib = B.load_library()
+    q, k, v = (fia_inputs.normal((4, n, s, 128), "bf16", 136, i).to(DEV) for i, (n, s) in enumerate(((64, 1), (1, 3000), (1, 3000))))
+    kw = dict(num_heads=64, num_key_value_heads=1, scale_value=0.1, input_layout="BNSD")
+    want, _ = fia.fia_decode_window(q, k, v, **kw)
+    lib.fia_debug_set_wait_limit_ns(1)
+    try:
+        short, _ = fia.fia_decode_window(q, k, v, **kw)
+        torch.cuda.synchronize()
+    finally:
+        lib.fia_debug_set_wait_limit_ns(0)
+    gave_up = short.isnan().flatten(1).any(1)
+    assert gave_up.any()
+    for b in range(4):
+        assert short[b].isnan().all() if gave_up[b] else torch.equal(short[b], want[b])
+    again, _ = fia.fia_decode_window(q, k, v, **kw)
+    assert torch.equal(again, want)
