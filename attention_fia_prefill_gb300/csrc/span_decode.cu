@@ -11,7 +11,7 @@
 // g heads x Q_S tokens: up to 32 here, more (and 17..32 with many keys) in
 // span_wide.cu.  Its keys are the 16-key tiles of the sinks and of [first row's
 // window, L): a list whose length the device knows.
-//   * Work: a cluster of 1..8 CTAs runs a unit, each CTA four warps.  A warp
+//   * Work: a cluster of 1..16 CTAs runs a unit, each CTA four warps.  A warp
 //     owns 16 rows (mma.sync m16n8k16); units of up to 16 rows give each warp
 //     keys of its own (tile v of the list belongs to group v mod groups), those
 //     of 17..32 pair the warps of a group over the same tiles, two a step.
@@ -33,7 +33,7 @@
 // Bound: HBM where spans are long (64 sequences x 4 tokens, window 4096: 163 us,
 // 95% of a copy's rate); where they are short the chain length -> page ids ->
 // keys -> join and code fetched for one use (16 sequences, window 1024: 14.5 us,
-// 59%; one sequence 6.3 us).
+// 59%; one sequence 6.2 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
 template <int D, bool BF16, int MT>
 cudaError_t launch_one(const SpanParams& p, cudaStream_t s) {
   using C = SpanCfg<D, MT>;
-  cudaError_t e = set_smem_once<span_decode_kernel<D, BF16, MT>>(C::kSmem);
+  cudaError_t e = prepare_span<span_decode_kernel<D, BF16, MT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   return launch_span(span_decode_kernel<D, BF16, MT>, p, p, kSpanThreads, C::kSmem, s);
 }
@@ -372,7 +372,8 @@ cudaError_t launch_one(const SpanParams& p, cudaStream_t s) {
 // CTAs of a unit, us: 16 sequences x 8 heads, window of 65 tiles 24.0, 17.8, 25.6,
 // 41.1; 64 x 8, 257 tiles 170, 193, 197, 273; 32 x 8, lengths up to 513 tiles
 // 133, 113, 106, 128.  Where the keys' limit is the tables' and not the window's
-// the lengths behind it vary.)
+// the lengths behind it vary.  Clusters of 16 where 8 were the most: one sequence
+// x 8 heads of 32768 keys 61.7 -> 37.6, of a window of 4096 11.7 -> 9.1.)
 constexpr int kSpanStart = 4;
 
 cudaError_t launch_span_decode(const SpanParams& params, int head_dim, bool bf16, int n_sm, cudaStream_t s) {
@@ -380,7 +381,7 @@ cudaError_t launch_span_decode(const SpanParams& params, int head_dim, bool bf16
   if (p.rows > 32) return cudaErrorInvalidValue;
   const int mt = p.rows <= 16 ? 1 : 2;
   const int64_t span = std::min<int64_t>(p.kv_max - p.base, int64_t(p.sink) + p.pre + p.q_tokens);
-  set_span_shape(p, cluster_ctas(int64_t(p.B) * p.N2, span / kSpanTile + 1, 4 / mt, kSpanStart,
+  set_span_shape(p, cluster_ctas(int64_t(p.B) * p.N2, p.rows, span / kSpanTile + 1, 4 / mt, kSpanStart,
                                  span < p.kv_max - p.base, (head_dim == 64 ? 4 : 2) * n_sm));
 #define FIA_SPAN(DD, BB) return mt == 1 ? launch_one<DD, BB, 1>(p, s) : launch_one<DD, BB, 2>(p, s)
   if (head_dim == 128) {

@@ -2,6 +2,7 @@
 // a CTA's groups, of the unit's CTAs and of a shared prefix, joined and written.
 #pragma once
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "paged.h"
@@ -9,7 +10,7 @@
 
 namespace fia {
 
-constexpr int kMostCtas = 8;         // CTAs of a unit (a portable cluster)
+constexpr int kMostCtas = 16;        // CTAs of a unit (a cluster; above 8 by leave of the kernel)
 
 // The cluster's barrier in halves: arrive releases this thread's writes, wait
 // acquires every CTA's.
@@ -168,13 +169,16 @@ __device__ __forceinline__ void span_join(const SpanParams& p, const float* ob, 
 // CTAs of a unit: those whose waves take the least time, a CTA costing its
 // groups' tiles and about `start` tiles more (launch, length, page ids, first
 // keys, join).  even: units have like lengths; else smaller shares even them out,
-// and up to a seventh more by this count is taken for them.
-inline int cluster_ctas(int64_t units, int64_t tiles, int groups, int start, bool even, int64_t slots) {
+// and up to a seventh more by this count is taken for them.  Joining 16 CTAs costs
+// about a tile for every 8 rows more than joining 8 (8 units, us with 8 and with
+// 16: 4 rows, 4096 keys 11.7, 9.1; 32 rows, 384 keys 6.3, 8.0; 64 rows, 4096 keys
+// 14.5, 15.9).
+inline int cluster_ctas(int64_t units, int rows, int64_t tiles, int groups, int start, bool even, int64_t slots) {
   int best = 1;
   int64_t least = 0;
   for (int cs = 1; cs <= kMostCtas; cs *= 2) {
     const int64_t waves = (units * cs + slots - 1) / slots;
-    const int64_t cost = waves * ((tiles + cs * groups - 1) / (cs * groups) + start);
+    const int64_t cost = waves * ((tiles + cs * groups - 1) / (cs * groups) + start + (cs > 8 ? rows / 8 : 0));
     if (cs == 1 || (even ? cost < least : cost * 7 < least * 8)) best = cs;
     if (cs == 1 || cost < least) least = cost;
   }
@@ -183,11 +187,27 @@ inline int cluster_ctas(int64_t units, int64_t tiles, int groups, int start, boo
 
 // What the launch adds to the parameters.
 inline void set_span_shape(SpanParams& p, int cs) {
-  p.lg_cs = cs == 8 ? 3 : cs / 2;
+  p.lg_cs = 0;
+  while (1 << p.lg_cs < cs) ++p.lg_cs;
   p.q_inv = 65536u / unsigned(p.q_tokens) + 1u;   // floor(r q_inv / 2^16) = r / q_tokens for r < 64, q_tokens <= 16
   p.lg_block = -1;
   for (int k = 4; k < 31; ++k)
     if (p.block_size == 1 << k) p.lg_block = k;
+}
+
+// Shared memory and clusters of 16, on the first launch on each device.
+template <auto Kernel>
+cudaError_t prepare_span(int smem) {
+  static std::atomic<unsigned long long> done{0};   // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
+  if ((done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // One cluster of CTAs per unit, let in while the kernel before it ends.

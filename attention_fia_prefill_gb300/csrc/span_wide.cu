@@ -2,7 +2,7 @@
 // rows, on the tcgen05 tensor cores.  mma.sync bounds such units: every warp
 // reads every tile's fragments from shared memory for 16 rows of its own.
 //
-//   * A unit (batch, kv head) is run by a cluster of 1..8 CTAs, two to an SM (one
+//   * A unit (batch, kv head) is run by a cluster of 1..16 CTAs, two to an SM (one
 //     chain softmax -> product a CTA); CTA r takes the 64-key tiles r, r + CTAs, ...
 //     of the visible span.
 //   * S = Q K^T has 128 TMEM lanes, of which a unit fills 17..64.  Q is laid
@@ -48,7 +48,8 @@ struct WideParams {
 constexpr int kKeys = 64;            // of a tile
 // Start cost of a CTA in tiles.  (1, 2, 4, 8 CTAs of a unit, us, 64 rows, D 128:
 // 128 units with 2000..4096 keys 55.0, 42.0, 49.5, 66.9; 64 units of 4096 keys
-// 51.9, 37.1, 30.3, 40.4; 256 units 84.9, 97.4, 117, 153.)
+// 51.9, 37.1, 30.3, 40.4; 256 units 84.9, 97.4, 117, 153.  16 instead of 8: one
+// unit of 30000 keys 61.1 -> 35.2.)
 constexpr int kWideStart = 10;
 
 template <int D, int R>
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
 template <int D, bool BF16, int R>
 cudaError_t launch_one(const WideParams& w, cudaStream_t s) {
   constexpr int smem = WideCfg<D, R>::kSmem;
-  cudaError_t e = set_smem_once<span_wide_kernel<D, BF16, R>>(smem);
+  cudaError_t e = prepare_span<span_wide_kernel<D, BF16, R>>(smem);
   if (e != cudaSuccess) return e;
   return launch_span(span_wide_kernel<D, BF16, R>, w, w.s, kWideThreads, smem, s);
 }
@@ -472,7 +473,8 @@ fia_status launch_span_wide(const SpanParams& p, int head_dim, bool bf16, int n_
   WideParams w;
   memset(&w, 0, sizeof(w));
   w.s = p;
-  set_span_shape(w.s, cluster_ctas(int64_t(p.B) * p.N2, visible_span(p) / kKeys + 1, 1, kWideStart, true, 2 * n_sm));
+  set_span_shape(w.s, cluster_ctas(int64_t(p.B) * p.N2, p.rows, visible_span(p) / kKeys + 1, 1, kWideStart, true,
+                                   2 * n_sm));
   const uint64_t e = 2, D = uint64_t(head_dim), g = uint64_t(p.group), Q = uint64_t(p.q_tokens);
   const uint64_t qd[5] = {D, Q, g, uint64_t(p.N2), uint64_t(p.B)};
   const uint64_t qs[4] = {uint64_t(p.q_ss) * e, uint64_t(p.q_sn) * e, uint64_t(p.q_sn) * g * e, uint64_t(p.q_sb) * e};
