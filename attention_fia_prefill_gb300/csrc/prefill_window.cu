@@ -20,15 +20,19 @@
 //     16) * 16 of them, tile B's first band tile (before its window, walked
 //     because tile A needs it) none, for which 16 are taken.  The products are
 //     cut to them;
-//   * the code is kept small (rolled loops, short waits, tiles on an edge of the
-//     window on a path of their own): it exceeds an SM's instruction cache, and
-//     with masks in the full tiles' path, or waits that report by themselves, the
-//     misses cost up to a third (cache hit rate 73% at 401 us, 94% at 305).
-// Ragged prompts (8 sequences of 256..4096, 32 heads, window 1024): 301 us, one
-// CTA per item 350; chunks of 2048 after contexts up to 14336, window 4096: 781
+//   * the code is kept small (rolled loops, short waits, one path for whole tiles
+//     and for those on an edge of the window, whose hidden columns come as bit
+//     masks): it exceeds an SM's instruction cache, and the misses cost up to a
+//     third (cache hit rate 73% at 401 us, 94% at 305);
+//   * registers move from the producer's and issuer's warps to the softmax's
+//     (setmaxnreg; 384 threads x 168 = 128 x 120 + 256 x 192): a few spilled ones
+//     in the softmax's loop cost 5%, 294 -> 275 us with a path of their own for
+//     edge tiles; without that path 258.
+// Ragged prompts (8 sequences of 256..4096, 32 heads, window 1024): 258 us, one
+// CTA per item 350; chunks of 2048 after contexts up to 14336, window 4096: 726
 // and 837 us.  Bound: the chain of a tile's step (products 1024 cycles, softmax
-// 1400, hand-over 600) with two tiles in flight: the tensor core works 66% of a
-// step inside an item, and an item's edges and output cost about six steps more.
+// 1300, hand-over 600) with two tiles in flight, and an item's first and last
+// steps and output, about 4 us.
 // The walk of an item: the tiles of the sinks that the band does not hold, then
 // the band's from tile A's first to tile B's last (tile A stops at its own).
 #include <algorithm>
@@ -62,7 +66,7 @@ struct WinCfg {
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kOffBar = kOffV + kStages * kTile;
   static constexpr int kSmem = kOffBar + 512 + 1024;
-  static constexpr int kThreads = 320;
+  static constexpr int kThreads = 384;
   static constexpr uint32_t kColO = 256;
 };
 
@@ -227,6 +231,7 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
 
   if (warp == 0) {
     // ------------------------------------------------------- items, producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     if (lane == 0) {
       tma_prefetch_desc(&p.tm_q);
       tma_prefetch_desc(&p.tm_k);
@@ -332,6 +337,7 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_f16(128, 0, BF16 ? 1 : 0, 0, 0);   // N is the step's
       constexpr uint32_t idesc_pv = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
@@ -466,9 +472,12 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
         wait(&bar->drain, 0, nullptr, kWaitLimitNs);
       }
     }
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
   } else {
     // ------------------------------------------------------------ softmax
-    const int t = (warp - 2) >> 2;              // 0: tile A, 1: tile B
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int t = (warp - 4) >> 2;              // 0: tile A, 1: tile B
     const int r = 32 * (warp & 3) + lane;
     const uint32_t lane_off = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t col_s = tmem + lane_off + t * 128;
@@ -501,8 +510,8 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
       // the row's position, and the warp's first one (lengths and pre are at
       // most 2^30)
       const int pos = it.kv_len - it.q_len + i, pos_0 = pos - lane;
-      // whole tiles for the warp: no key past its first row's last, none before
-      // its last row's window
+      // whole tiles for the warp (no key past its first row's last, none before
+      // its last row's window) start in [full_lo, full_hi]
       const int full_hi = min(it.kv_len - 1, pos_0) - (kTileN - 1), full_lo = pos_0 + 31 - p.band_pre;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++c) {
@@ -513,127 +522,80 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
         }
         tc_fence_after();
         const bool ragged = kv0 + kTileN > kv_len && j >= clear_from;
-        if (kv0 > full_hi || kv0 < full_lo) {
-          // A tile on an edge of the warp's rows, 32 columns at a time: those
-          // that no row sees are neither loaded nor exponentiated (P = 0; none of
-          // them seen: the max, the sum and O stay as they are).  Two passes over
-          // S, so that this path needs few registers and the other one no branch.
-          const int lim = min(kv_len - 1, pos), lim_31 = min(kv_len - 1, pos_0 + 31), lo_0 = pos_0 - p.band_pre;
-          auto hid = [&](int k0) -> bool { return k0 > lim_31 || (k0 >= p.sink && k0 + 31 < lo_0); };
-          // columns [0, sinks) and [from, to] of the piece are the row's
-          auto piece = [&](int q, uint32_t (&su)[32]) {
-            tmem_ld32(col_s + 32 * q, su);
-            const int k0 = kv0 + 32 * q, to = lim - k0, from = pos - p.band_pre - k0, sinks = min(p.sink - k0, to + 1);
-            tmem_wait_ld(su);
+        const bool edge = kv0 > full_hi || kv0 < full_lo;
+        // bit e: column k0 + e is hidden from the row
+        auto hidden = [&](int k0) -> uint32_t {
+          const int to = min(kv_len - 1, pos) - k0, from = pos - p.band_pre - k0, sinks = min(p.sink - k0, to + 1);
+          const uint32_t past = to < 0 ? 0xffffffffu : to >= 31 ? 0u : 0xfffffffeu << to;
+          const uint32_t before = from <= 0 ? 0u : from >= 32 ? 0xffffffffu : ~(0xffffffffu << from);
+          const uint32_t sink = sinks <= 0 ? 0u : sinks >= 32 ? 0xffffffffu : ~(0xffffffffu << sinks);
+          return past | (before & ~sink);
+        };
+        uint32_t su[4][32];
+        tmem_ld32(col_s, su[0]);
+        tmem_ld32(col_s + 32, su[1]);
+        tmem_ld32(col_s + 64, su[2]);
+        tmem_ld32(col_s + 96, su[3]);
+        tmem_wait_ld(su[0]);
+        tmem_regs_after_wait(su[1]);
+        tmem_regs_after_wait(su[2]);
+        tmem_regs_after_wait(su[3]);
+        if (edge) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t hide = hidden(kv0 + 32 * q);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (e > to || (e < from && e >= sinks)) su[e] = __float_as_uint(-INFINITY);
-          };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            if (hid(kv0 + 32 * q)) continue;
-            uint32_t su[32];
-            piece(q, su);
-            float a[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = fmaxf(__uint_as_float(su[e]), __uint_as_float(su[4 + e]));
-#pragma unroll
-            for (int g = 8; g < 32; g += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) a[e] = fmax3(a[e], __uint_as_float(su[g + e]), __uint_as_float(su[g + 4 + e]));
-            top = fmax3(top, fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+              if ((hide >> e) & 1u) su[q][e] = __float_as_uint(-INFINITY);
           }
-          const float m_new = fmaxf(m, top * sl2);
-          const float m_use = (m == -INFINITY || m_new > m + 8.f) ? m_new : m;   // as below
-          const float alpha = (m_use == m) ? 1.f : fast_exp2(m - m_use);
-          const float mo = (m_use == -INFINITY) ? 0.f : m_use;
-          uint64_t acc2[2] = {0ull, 0ull};   // summed in the whole tiles' order
-          // (P of a piece takes columns of pieces that have been read)
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t u[16];
-            if (hid(kv0 + 32 * q)) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = 0u;
-            } else {
-              uint32_t su[32];
-              piece(q, su);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float y0 = fast_exp2(fmaf(__uint_as_float(su[2 * e]), sl2, -mo));
-                const float y1 = fast_exp2(fmaf(__uint_as_float(su[2 * e + 1]), sl2, -mo));
-                acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(y0, y1));
-                u[e] = pack2(y0, y1, BF16);
-              }
-            }
-            tmem_st16(col_s + q * 16, u);
-          }
-          float s0, s1;
-          f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
-          l = l * alpha + (s0 + s1);
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
-          m = m_use;
-        } else {
-          // S in two halves: the second half's load is in flight while the
-          // first half is masked and reduced
-          uint32_t su[4][32];
-          tmem_ld32(col_s, su[0]);
-          tmem_ld32(col_s + 32, su[1]);
-          tmem_wait_ld(su[0]);
-          tmem_regs_after_wait(su[1]);
-          tmem_ld32(col_s + 64, su[2]);
-          tmem_ld32(col_s + 96, su[3]);
-          float* x = reinterpret_cast<float*>(&su[0][0]);
-          float a[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmax3(x[q], x[8 + q], x[16 + q]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[24 + q], x[32 + q]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[40 + q], x[48 + q]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmaxf(a[q], x[56 + q]);
-          tmem_wait_ld(su[2]);
-          tmem_regs_after_wait(su[3]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[64 + q], x[72 + q]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[80 + q], x[88 + q]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[96 + q], x[104 + q]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[112 + q], x[120 + q]);
-          const float m_tile = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
-          const float m_new = fmaxf(m, m_tile * sl2);
-          // Keep a stale max unless it grows by more than 8 (log2 units): p <=
-          // 2^8 stays exact in fp32 and representable in bf16 / f16.
-          const float m_use = (m == -INFINITY || m_new > m + 8.f) ? m_new : m;
-          const float alpha = (m_use == m) ? 1.f : fast_exp2(m - m_use);
-          const float mo = (m_use == -INFINITY) ? 0.f : m_use;
-          const uint64_t sc2 = f2_pack(sl2, sl2), nmo2 = f2_pack(-mo, -mo);
-          uint64_t acc2[2] = {0ull, 0ull};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t u[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float y0, y1;
-              f2_unpack(f2_fma(f2_pack(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), sc2, nmo2), y0, y1);
-              y0 = fast_exp2(y0);
-              y1 = fast_exp2(y1);
-              acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(y0, y1));
-              u[e] = pack2(y0, y1, BF16);   // the weights' one rounding; their sum is not rounded
-            }
-            tmem_st16(col_s + q * 16, u);
-          }
-          float s0, s1;
-          f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
-          l = l * alpha + (s0 + s1);
-          // O_t holds the step before's P V: this S was issued after it
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
-          m = m_use;
         }
+        float* x = reinterpret_cast<float*>(&su[0][0]);
+        float a[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmax3(x[q], x[8 + q], x[16 + q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[24 + q], x[32 + q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[40 + q], x[48 + q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmaxf(a[q], x[56 + q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[64 + q], x[72 + q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[80 + q], x[88 + q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[96 + q], x[104 + q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] = fmax3(a[q], x[112 + q], x[120 + q]);
+        const float m_tile = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+        const float m_new = fmaxf(m, m_tile * sl2);
+        // Keep a stale max unless it grows by more than 8 (log2 units): p <=
+        // 2^8 stays exact in fp32 and representable in bf16 / f16.
+        const float m_use = (m == -INFINITY || m_new > m + 8.f) ? m_new : m;
+        const float alpha = (m_use == m) ? 1.f : fast_exp2(m - m_use);
+        const float mo = (m_use == -INFINITY) ? 0.f : m_use;
+        const uint64_t sc2 = f2_pack(sl2, sl2), nmo2 = f2_pack(-mo, -mo);
+        uint64_t acc2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float y0, y1;
+            f2_unpack(f2_fma(f2_pack(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), sc2, nmo2), y0, y1);
+            y0 = fast_exp2(y0);
+            y1 = fast_exp2(y1);
+            acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(y0, y1));
+            u[e] = pack2(y0, y1, BF16);   // the weights' one rounding; their sum is not rounded
+          }
+          tmem_st16(col_s + q * 16, u);
+        }
+        float s0, s1;
+        f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
+        l = l * alpha + (s0 + s1);
+        // O_t holds the step before's P V: this S was issued after it
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale_o(alpha);
+        m = m_use;
         if (ragged) {
           // rows of V past the batch's keys may hold anything, and 0 * NaN is
           // NaN: cleared before the first P V that reads the tile
@@ -677,7 +639,7 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
         using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
         const int64_t row = int64_t(it.q_row0) + t * kTileM + r, ob = is_tnd ? 0 : it.b;
         T* orow = reinterpret_cast<T*>(p.out) + ob * p.out_sb + row * p.out_ss + int64_t(it.h) * p.out_sn;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t u[32];
           if (n > 0) {
