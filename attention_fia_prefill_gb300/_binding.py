@@ -30,7 +30,7 @@ EXPORTS = [
     "fia_decode", "bsa_get_workspace_size", "bsa_forward", "bsa_fp8_get_workspace_size", "bsa_forward_fp8",
     "fia_device_status", "fia_status_string",
     "fia_last_error", "fia_profile_next_call", "fia_debug_set_wait_limit_ns", "fia_debug_set_decode_path", "fia_decode_no_alloc",
-    "fia_debug_plan_decode", "fia_block_table_append", "fia_cache_write", "fia_decode_window",
+    "fia_debug_set_prefix_path", "fia_debug_plan_decode", "fia_block_table_append", "fia_cache_write", "fia_decode_window",
     "fia_prefill_window_get_workspace_size", "fia_prefill_window",
     "fia_decode_shared_prefix_get_workspace_size", "fia_decode_shared_prefix",
 ]
@@ -112,6 +112,8 @@ def load_library(path: str | None = None):
     lib.fia_profile_next_call.restype = None
     lib.fia_debug_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.fia_debug_set_wait_limit_ns.restype = None
+    lib.fia_debug_set_prefix_path.argtypes = [ctypes.c_int32]
+    lib.fia_debug_set_prefix_path.restype = None
     lib.fia_debug_set_decode_path.argtypes = [ctypes.c_int]
     lib.fia_debug_set_decode_path.restype = None
     lib.fia_decode_no_alloc.argtypes = [T, T, T, T, T, T, T, P, T, T, vp]

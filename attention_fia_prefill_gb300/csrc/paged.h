@@ -54,7 +54,9 @@ struct SpanParams {
   int kv_max;                     // lengths are clamped to [0, kv_max]
   int B, N1, N2, group, q_tokens, rows;
   int pre, sink, base;
+  int shared;                     // keys below come from the table's first row
   float scale_log2;
+  DevStatus status;               // word nullable; stamped where n_parts is 0
   // partial results to join (the shared prefix): O (not divided by its sum)
   // [n_parts][B * N1 * q_tokens][D], (max in log2 units, sum) likewise, row
   // (b * N1 + head) * q_tokens + token

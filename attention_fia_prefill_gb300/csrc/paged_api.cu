@@ -2,6 +2,7 @@
 // validation and launches.  Lengths stay on the device; nothing here waits for
 // the GPU or copies to it.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstring>
@@ -292,6 +293,22 @@ fia_status window_prefill(const fia_tensor* q, const fia_tensor* k, const fia_te
   return FIA_OK;
 }
 
+std::atomic<int> g_prefix_path{0};   // fia_debug_set_prefix_path
+
+// Whether the prefix gets a kernel of its own: where reading it for every
+// sequence costs more than that kernel's start, partial results (which grow with
+// a unit's rows) and join.  (us, apart and by every sequence, by the bytes read
+// again: 4 rows, 6 MB 12.8, 7.6; 24 MB 14.4, 12.6; 30 MB 11.9, 10.5; 56 MB 12.2,
+// 13.7; 120 MB 13.4, 22.7; 32 rows, 14 MB 18.7, 10.7; 56 MB 20.4, 15.8; 120 MB 25.2,
+// 22.6; 248 MB 34.8, 35.5.  Of a long prefix a sequence's few CTAs read too much each:
+// 8192 keys, one kv head, 4 MB 10.5, 12.2.)
+bool prefix_apart(const SpanParams& p, int64_t prefix, int64_t D) {
+  const int path = g_prefix_path.load(std::memory_order_relaxed);
+  if (prefix == 0 || p.B < 2) return false;   // one sequence shares with nobody
+  if (path != 0) return path == 1;
+  return prefix > 4096 || (p.B - 1) * prefix * p.N2 * D * 4 > (int64_t(16 + 4 * p.rows) << 20);
+}
+
 // How fia_decode_shared_prefix cuts its work.
 struct PrefixPlan {
   bool split_off = false;   // a kernel for the prefix, joined by the decode of the rest
@@ -498,6 +515,8 @@ fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor* key, co
                     "window prefill launch");
 }
 
+void fia_debug_set_prefix_path(int32_t path) { g_prefix_path.store(path, std::memory_order_relaxed); }
+
 fia_status fia_decode_shared_prefix_get_workspace_size(const fia_tensor* query, const fia_tensor* key_cache,
                                                        const fia_tensor* value_cache, const fia_tensor* block_table,
                                                        const fia_tensor* actual_seq_kvlen, const fia_params* params,
@@ -531,8 +550,9 @@ fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* k
   const bool bf16 = query->dtype == FIA_DTYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  if (!w.split_off) {
-    FIA_TRY(cuda_check(cudaMemsetAsync(base, 0, 8, s), "status reset"));
+  if (!w.split_off || !prefix_apart(p, shared_prefix_len, D)) {
+    p.status = make_status(workspace);
+    p.shared = p.kv_max == 0 ? 0 : int(shared_prefix_len);
     return run_profiled(p, D, bf16, n_sm, s);
   }
   PrefillParams pp;
@@ -575,6 +595,7 @@ fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* k
   pp.status = make_status(workspace);
   FIA_TRY(cuda_check(profiled(s, [&] { return launch_prefill_pair(pp, int(D), int(D), bf16, kPrefix, s); }),
                      "prefix launch"));
+  p.status = pp.status;
   p.base = int(shared_prefix_len);
   p.part_o = pp.part_o;
   p.part_ml = pp.part_ml;

@@ -119,7 +119,10 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
   if (lg != 0) cluster_arrive();   // (waited for before the join's first remote store: every CTA runs by then)
   // Behind a prefix kernel, which lets this one go once everything before both
   // is complete, only the join has to wait for it.
-  if (p.n_parts == 0) grid_dep_wait();
+  if (p.n_parts == 0) {
+    grid_dep_wait();
+    if (p.status.word != nullptr && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) status_stamp(p.status);
+  }
   // Length, page ids and keys wait for one another: the length first, and
   // without a window, when they do not depend on it, the page ids; the queries
   // load meanwhile.
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kSpanThreads, SpanCfg<D, MT>::kResident) span_
     if (p.block_table == nullptr) return int64_t(b) * p.blk_stride + int64_t(j) * p.row_stride;
     const int page = p.lg_block >= 0 ? j >> p.lg_block : j / p.block_size;
     if (page >= p.table_stride) return -1;
-    const int id = p.block_table[int64_t(b) * p.table_stride + page];
+    const int id = p.block_table[(j < p.shared ? 0 : int64_t(b) * p.table_stride) + page];
     if (id < 0 || id >= p.n_blocks) return -1;
     return int64_t(id) * p.blk_stride + int64_t(j - page * p.block_size) * p.row_stride;
   };
@@ -382,7 +385,7 @@ cudaError_t launch_span_decode(const SpanParams& params, int head_dim, bool bf16
   const int mt = p.rows <= 16 ? 1 : 2;
   const int64_t span = std::min<int64_t>(p.kv_max - p.base, int64_t(p.sink) + p.pre + p.q_tokens);
   set_span_shape(p, cluster_ctas(int64_t(p.B) * p.N2, p.rows, span / kSpanTile + 1, 4 / mt, kSpanStart,
-                                 span < p.kv_max - p.base, (head_dim == 64 ? 4 : 2) * n_sm));
+                                 span < p.kv_max - p.base, head_dim == 64 ? 4 : 2, n_sm));
 #define FIA_SPAN(DD, BB) return mt == 1 ? launch_one<DD, BB, 1>(p, s) : launch_one<DD, BB, 2>(p, s)
   if (head_dim == 128) {
     if (bf16) FIA_SPAN(128, true);

@@ -172,11 +172,13 @@ __device__ __forceinline__ void span_join(const SpanParams& p, const float* ob, 
 // and up to a seventh more by this count is taken for them.  Joining 16 CTAs costs
 // about a tile for every 8 rows more than joining 8 (8 units, us with 8 and with
 // 16: 4 rows, 4096 keys 11.7, 9.1; 32 rows, 384 keys 6.3, 8.0; 64 rows, 4096 keys
-// 14.5, 15.9).
-inline int cluster_ctas(int64_t units, int rows, int64_t tiles, int groups, int start, bool even, int64_t slots) {
+// 14.5, 15.9), and is not done where SMs would share such clusters (16 units of 4
+// rows and 32768 keys 69.7, 73.2).
+inline int cluster_ctas(int64_t units, int rows, int64_t tiles, int groups, int start, bool even, int per_sm, int n_sm) {
+  const int64_t slots = int64_t(per_sm) * n_sm;
   int best = 1;
   int64_t least = 0;
-  for (int cs = 1; cs <= kMostCtas; cs *= 2) {
+  for (int cs = 1; cs <= (units * kMostCtas <= n_sm ? kMostCtas : kMostCtas / 2); cs *= 2) {
     const int64_t waves = (units * cs + slots - 1) / slots;
     const int64_t cost = waves * ((tiles + cs * groups - 1) / (cs * groups) + start + (cs > 8 ? rows / 8 : 0));
     if (cs == 1 || (even ? cost < least : cost * 7 < least * 8)) best = cs;

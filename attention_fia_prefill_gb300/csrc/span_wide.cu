@@ -19,8 +19,8 @@
 //   * Boxes that no row sees are not read (coordinates outside the tensor: zeros);
 //     rows of V that no row sees inside a box are cleared before the product
 //     (0 * NaN would reach the sums).
-//   * A wait that runs out leaves NaN in the unit's outputs: the call has no
-//     workspace to report in.
+//   * A wait that runs out leaves NaN in the unit's outputs (fia_decode_window has
+//     no workspace to report in) and FIA_ERR_TIMEOUT in a status word, if any.
 // Bound: HBM with many units (256 of 64 rows and 4096 keys: 84.8 us, 96% of a
 // copy's rate; 512 of 32 rows, window 2048: 96 us, 85%); with fewer the chain of a
 // tile, 0.6 us for 32 KB (128 units of 64 rows, 2000 to 4096 keys: 42 us, 73%;
@@ -165,7 +165,10 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
   grid_dep_launch();               // (TMEM is taken: a kernel let in now cannot hold it and wait for this one)
-  if (p.n_parts == 0) grid_dep_wait();
+  if (p.n_parts == 0) {
+    grid_dep_wait();
+    if (p.status.word != nullptr && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) status_stamp(p.status);
+  }
 
   int len = p.kv_max;
   if (p.kv_len != nullptr)
@@ -210,7 +213,8 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
       id = b;
       if (p.block_table != nullptr) {
         const int page = p.lg_block >= 0 ? k0 >> p.lg_block : k0 / p.block_size;
-        id = p.block_table[int64_t(b) * p.table_stride + page];   // (k0 < L: a column of the table)
+        // (k0 < L: a column of the table)
+        id = p.block_table[(k0 < p.shared ? 0 : int64_t(b) * p.table_stride) + page];
         row = k0 - page * p.block_size;
       }
     };
@@ -433,6 +437,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
   if (*abort_flag != 0) {
     const float nan = __uint_as_float(0x7fc00000u);
     for (int e = threadIdx.x; e < 128; e += kWideThreads) ml[e] = make_float2(nan, nan);
+    if (p.status.word != nullptr && threadIdx.x == 0) status_raise(p.status, 10u /* FIA_ERR_TIMEOUT */);
   }
   span_join<D, BF16, R, C::kGroups, kWideThreads>(p, reinterpret_cast<const float*>(smem + C::kOffO), ml,
                                                   smem + C::kOffIn, lg, rank, b, kvh);
@@ -474,7 +479,7 @@ fia_status launch_span_wide(const SpanParams& p, int head_dim, bool bf16, int n_
   memset(&w, 0, sizeof(w));
   w.s = p;
   set_span_shape(w.s, cluster_ctas(int64_t(p.B) * p.N2, p.rows, visible_span(p) / kKeys + 1, 1, kWideStart, true,
-                                   2 * n_sm));
+                                   2, n_sm));
   const uint64_t e = 2, D = uint64_t(head_dim), g = uint64_t(p.group), Q = uint64_t(p.q_tokens);
   const uint64_t qd[5] = {D, Q, g, uint64_t(p.N2), uint64_t(p.B)};
   const uint64_t qs[4] = {uint64_t(p.q_ss) * e, uint64_t(p.q_sn) * e, uint64_t(p.q_sn) * g * e, uint64_t(p.q_sb) * e};

@@ -443,7 +443,8 @@ FIA_API fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor*
 /* ------------------------------------------------------------------------
  * fia_decode_shared_prefix: incremental attention for a batch whose sequences
  * begin with the same keys.  The result is fia_decode_window's without a
- * window; the prefix's keys and values are read once for the whole batch.
+ * window; the prefix's keys and values are read once for the whole batch (by
+ * every sequence where they are so few that this is faster).
  *   query, key_cache, value_cache, block_table, actual_seq_kvlen (the whole
  *          lengths, prefix and new tokens among them), attention_out,
  *          softmax_lse: as fia_decode_window with paged key/value;
@@ -493,6 +494,12 @@ FIA_API void fia_profile_next_call(void* start_event, void* stop_event);
  * the default.  A limit far below a kernel's run time makes its calls fail:
  * meant only for tests of that path. */
 FIA_API void fia_debug_set_wait_limit_ns(uint64_t ns);
+
+/* How fia_decode_shared_prefix reads the prefix: 0 (the default) by the sizes,
+ * 1 always by a kernel of its own, 2 never (each sequence reads it).  Applies
+ * to calls launched afterwards from any thread.  Meant for tests that compare
+ * the two. */
+FIA_API void fia_debug_set_prefix_path(int32_t path);
 
 /* Selects the decode kernel for units (batch, kv head) of at most 16 query
  * rows with head_dim 128: 0 (the default) the warp-level kernel (mma.sync per

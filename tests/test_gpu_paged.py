@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import fia_inputs
+from attention_fia_prefill_gb300 import _binding
 from oracle import paged_oracle as po
 from oracle.fia_oracle import f64
 
@@ -422,6 +423,15 @@ def _prefix(fia, own_lens, P, n1, n2, D, Q=1, bs=128, dt="bf16", kv="BNBD", layo
     po.assert_close(o, lse, po.decode(c.q, rows, lens, 1 << 40, 0, scale))
     again, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=P, **kw)
     assert torch.equal(out, again)
+    for path in (1, 2):       # the prefix by a kernel of its own, and by every sequence's
+        lib = _binding.load_library()
+        lib.fia_debug_set_prefix_path(path)
+        try:
+            o, l = fia.fia_decode_shared_prefix(*args, shared_prefix_len=P, **kw)
+        finally:
+            lib.fia_debug_set_prefix_path(0)
+        o = o.reshape(B, Q, n1, D).transpose(1, 2) if layout != "BNSD" else o
+        po.assert_close(o, l, po.decode(c.q, rows, lens, 1 << 40, 0, scale))
     return out, lse, args, kw
 
 
@@ -469,6 +479,14 @@ def test_prefix_reads_the_first_row_only(fia):
     kw["block_table"][1:, :3] = -9
     o2, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=384, **kw)
     assert torch.equal(out, o2)
+    _binding.load_library().fia_debug_set_prefix_path(1)
+    try:
+        o3, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=384, **kw)
+        kw["block_table"][1:, :3] = kw["block_table"][0, :3]
+        o4, _ = fia.fia_decode_shared_prefix(*args, shared_prefix_len=384, **kw)
+    finally:
+        _binding.load_library().fia_debug_set_prefix_path(0)
+    assert torch.equal(o3, o4)
 
 
 def test_prefix_status_and_workspace(fia):
