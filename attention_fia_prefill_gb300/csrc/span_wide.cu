@@ -165,10 +165,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
   grid_dep_launch();               // (TMEM is taken: a kernel let in now cannot hold it and wait for this one)
-  if (p.n_parts == 0) {
-    grid_dep_wait();
-    if (p.status.word != nullptr && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) status_stamp(p.status);
-  }
+  if (p.n_parts == 0) grid_dep_wait();
 
   int len = p.kv_max;
   if (p.kv_len != nullptr)
@@ -437,10 +434,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
   if (*abort_flag != 0) {
     const float nan = __uint_as_float(0x7fc00000u);
     for (int e = threadIdx.x; e < 128; e += kWideThreads) ml[e] = make_float2(nan, nan);
-    if (p.status.word != nullptr && threadIdx.x == 0) status_raise(p.status, 10u /* FIA_ERR_TIMEOUT */);
+    if (threadIdx.x == 0) status_raise(p.status, 10u /* FIA_ERR_TIMEOUT */);
   }
   span_join<D, BF16, R, C::kGroups, kWideThreads>(p, reinterpret_cast<const float*>(smem + C::kOffO), ml,
                                                   smem + C::kOffIn, lg, rank, b, kvh);
+  // (a word that this call has raised stays)
+  if (p.n_parts == 0 && (threadIdx.x | blockIdx.x | blockIdx.y) == 0) status_stamp(p.status);
 }
 
 template <int D, bool BF16, int R>

