@@ -146,11 +146,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
   WorkItem it;
   BatchInfo bi;
   if constexpr (MODE == kPrefix) {
-    // The decode of the sequences' own keys needs no result of this kernel
-    // before its join, but what came before both has to be complete: it is let
-    // go after the wait.
     grid_dep_wait();
-    grid_dep_launch();
     // splits outermost: the pairs of rows that read the same keys are neighbours
     const int x = blockIdx.x / p.n_pairs;
     it.cost = x / p.num_kv_heads;                  // the split
@@ -249,6 +245,10 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  // The decode of the sequences' own keys needs no result of this kernel before
+  // its join, but what came before both has to be complete: it is let go after
+  // the wait, and with TMEM taken (a kernel let in may hold its own and wait).
+  if constexpr (MODE == kPrefix) grid_dep_launch();
 
   const bool is_tnd = p.is_tnd != 0;
   const int q_row0 = is_tnd ? bi.q_start + q0 : q0;

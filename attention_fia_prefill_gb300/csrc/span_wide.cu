@@ -150,26 +150,31 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(&bar->tmem, C::kTmem);
-    tmem_relinquish();
-  }
   // the copies' rows behind the unit's: zeros
   for (int e = threadIdx.x; e < C::kGroups * (R - p.rows) * (D / 8); e += kWideThreads) {
     const int row = e / (D / 8), c = e % (D / 8), g = row / (R - p.rows), at = g * R + p.rows + row % (R - p.rows);
     *reinterpret_cast<uint4*>(smem + C::kOffQ + (c / 8) * C::kBoxQ + at * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
+  // Behind a prefix kernel, which lets this one go once everything before both
+  // is complete, only the join has to wait for it.
+  if (p.n_parts == 0) grid_dep_wait();
+  int len = p.kv_max;
+  if (p.kv_len != nullptr)
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(len) : "l"(p.kv_len + b) : "memory");
+  // TMEM is held neither while this kernel waits for one before it, whose CTAs
+  // may yet have to get theirs, nor wanted once it has let the next one in, which
+  // may hold its own and wait for this one: either could wait forever.
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem, C::kTmem);
+    tmem_relinquish();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
-  grid_dep_launch();               // (TMEM is taken: a kernel let in now cannot hold it and wait for this one)
-  if (p.n_parts == 0) grid_dep_wait();
+  grid_dep_launch();
 
-  int len = p.kv_max;
-  if (p.kv_len != nullptr)
-    asm volatile("ld.global.b32 %0, [%1];" : "=r"(len) : "l"(p.kv_len + b) : "memory");
   const int L = min(max(len, 0), p.kv_max);
   const int first = L - p.q_tokens;               // position of token 0 (may be negative: tokens that see nothing)
   // the tiles that hold a key some row may see: the sinks' and the window's
