@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
   volatile int* abort_flag = &bar->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) status_stamp(p.status);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar->q_full[t], 1);
       mbar_init(&bar->p_full[t][0], 4);
@@ -219,6 +218,11 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // The launch overlaps the end of the kernel before; this one lets the next go
+  // by ending (let go at the start, its CTAs cost 3%).  TMEM is taken after the
+  // wait: no kernel waits with it in hand.
+  grid_dep_wait();
+  if (threadIdx.x == 0 && blockIdx.x == 0) status_stamp(p.status);
   if (warp == 1) {
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
@@ -685,8 +689,8 @@ template <int D, bool BF16>
 cudaError_t launch_one(const PrefillParams& p, int n_sm, cudaStream_t s) {
   cudaError_t e = set_smem_once<prefill_window_kernel<D, BF16>>(WinCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  prefill_window_kernel<D, BF16><<<std::min(p.n_items, n_sm), WinCfg<D>::kThreads, WinCfg<D>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(prefill_window_kernel<D, BF16>, dim3(unsigned(std::min(p.n_items, n_sm))), WinCfg<D>::kThreads,
+                      WinCfg<D>::kSmem, s, p);
 }
 
 }  // namespace
