@@ -395,7 +395,8 @@ FIA_API fia_status fia_cache_write(const fia_tensor* key, int64_t key_token_stri
  *   Rows that see no key (p < 0: a padded batch) give 0 and +inf.  With several
  *          new tokens the values (not scores) of a key that only some of them
  *          see enter the others' sums with a weight of 0: they must be finite.
- *   No workspace.
+ *   No workspace, and so no status word: a bounded wait that runs out (units of
+ *          more than 16 rows) leaves NaN in its unit's rows.
  * ------------------------------------------------------------------------ */
 FIA_API fia_status fia_decode_window(const fia_tensor* query, const fia_tensor* key, const fia_tensor* value,
                              const fia_tensor* block_table, const fia_tensor* actual_seq_kvlen,
