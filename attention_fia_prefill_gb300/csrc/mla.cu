@@ -350,7 +350,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1) mla_kernel(c
         }
       }
     }
-    if (lane == 0 && *abort_flag) {
+    if (lane == 0) {
+      // Every copy lands before the CTA exits, also where another role gives up
+      // after these loads have all been issued (nothing waits for this lane).
       for (int s = 0; s < kKS && s < j; ++s) {
         const int last = j - 1 - ((j - 1 - s) % kKS);
         mbar_wait_lean(&bar->k_full[s], uint32_t(last / kKS) & 1u, nullptr, p.status);
@@ -377,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1) mla_kernel(c
         }
         ++issued;
       }
-      if (*abort_flag && issued > 0) mbar_wait_lean(&bar->q_full, uint32_t(issued - 1) & 1u, nullptr, p.status);
+      if (issued > 0) mbar_wait_lean(&bar->q_full, uint32_t(issued - 1) & 1u, nullptr, p.status);
     }
   } else if (warp == 5) {
     // ------------------------------------------------------- MMA issuer

@@ -154,13 +154,13 @@ __global__ void __launch_bounds__(192, 1) prefill_kernel(const __grid_constant__
         for (int c = 0; c < C::kChunks; ++c)
           tma_load_4d(vs + c * C::kBoxBytes, &p.tm_v, &v_full[s], c * 64, kv_row0 + t * kTileN, kvh, b_coord);
       }
-      // On an abort, let every copy already issued land before the CTA exits.
-      if (*abort_flag) {
-        for (int s = 0; s < S && s < j; ++s) {
-          const int last = j - 1 - ((j - 1 - s) % S);   // last tile issued into stage s
-          mbar_wait(&k_full[s], (last / S) & 1, nullptr, p.status);
-          mbar_wait(&v_full[s], (last / S) & 1, nullptr, p.status);
-        }
+      // Every copy lands before the CTA exits, also where another role gives up
+      // after these loads have all been issued (nothing waits for this lane).
+      mbar_wait(q_full, 0, nullptr, p.status);
+      for (int s = 0; s < S && s < j; ++s) {
+        const int last = j - 1 - ((j - 1 - s) % S);   // last tile issued into stage s
+        mbar_wait(&k_full[s], (last / S) & 1, nullptr, p.status);
+        mbar_wait(&v_full[s], (last / S) & 1, nullptr, p.status);
       }
     }
   } else if (warp == 1) {

@@ -349,17 +349,16 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
             }
         }
       }
-      if (*abort_flag) {
-        // let every copy in flight land before the CTA exits
-        mbar_wait_lean(q_full, 0, nullptr, p.status);
-        for (int s = 0; s < KS && s < nk; ++s) {
-          const int last = nk - 1 - ((nk - 1 - s) % KS);
-          mbar_wait_lean(&k_full[s], (last / KS) & 1, nullptr, p.status);
-        }
-        for (int s = 0; s < VS && s < nv; ++s) {
-          const int last = nv - 1 - ((nv - 1 - s) % VS);
-          mbar_wait_lean(&v_full[s], (last / VS) & 1, nullptr, p.status);
-        }
+      // Every copy lands before the CTA exits, also where another role gives up
+      // after these loads have all been issued (nothing waits for this lane).
+      mbar_wait_lean(q_full, 0, nullptr, p.status);
+      for (int s = 0; s < KS && s < nk; ++s) {
+        const int last = nk - 1 - ((nk - 1 - s) % KS);
+        mbar_wait_lean(&k_full[s], (last / KS) & 1, nullptr, p.status);
+      }
+      for (int s = 0; s < VS && s < nv; ++s) {
+        const int last = nv - 1 - ((nv - 1 - s) % VS);
+        mbar_wait_lean(&v_full[s], (last / VS) & 1, nullptr, p.status);
       }
     }
   } else if (warp == 1) {

@@ -330,8 +330,9 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
         ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
       }
     }
-    if (lane == 0 && *abort_flag) {
-      // let every copy in flight land before the CTA exits
+    if (lane == 0) {
+      // Every copy lands before the CTA exits, also where another role gives up
+      // after these loads have all been issued (nothing waits for this lane).
       if (nqa > 0) wait(&bar->q_full[0], (nqa - 1) & 1, nullptr, kWaitLimitNs);
       if (nqb > 0) wait(&bar->q_full[1], (nqb - 1) & 1, nullptr, kWaitLimitNs);
       for (int s = 0; s < ST; ++s) {

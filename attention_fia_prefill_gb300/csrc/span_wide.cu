@@ -256,8 +256,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
       id = id_n;
     }
     __syncwarp();
-    if (lane == 0 && *abort_flag != 0) {
-      // let every copy in flight land before the CTA exits
+    if (lane == 0) {
+      // Every copy lands before the CTA exits, also where another role gives up
+      // after these loads have all been issued (nothing waits for this lane).
       if (n > 0) wait(&bar->q_full, 0, nullptr, kWaitLimitNs);
       for (int s = 0; s < ST; ++s) {
         if (nk > s) wait(&bar->k_full[s], ((nk - 1 - (nk - 1 - s) % ST) / ST) & 1, nullptr, kWaitLimitNs);
