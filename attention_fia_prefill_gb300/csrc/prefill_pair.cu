@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
   uint64_t* pva_done = bars + 20;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 21);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
+  uint64_t* drain = bars + 23;     // after an abort
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WorkItem it;
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       mbar_init(&pb_full[t], 4);
     }
     mbar_init(pva_done, 1);
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -438,8 +440,13 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
         }
       }
       // Every MMA issued has finished before TMEM goes: the latest commit
-      // tracks them all (the one before it on the same barrier has completed).
+      // tracks them all (the one before it on the same barrier has completed),
+      // but for tile A's P V, which an abort leaves without one.
       if (last_bar != nullptr) mbar_wait_lean(last_bar, last_parity, nullptr, p.status);
+      if (!ok) {
+        mma_commit(drain);
+        mbar_wait_lean(drain, 0, nullptr, p.status);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -687,6 +694,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       m = m_use;
     }
     if (MODE == kMask) cp_async_wait_all();   // no copy into the slot outlives the loop
+    if (!ok) tmem_wait_st();                  // no store to TMEM is pending when it goes
     // ------------------------------------------------------------ epilogue
     if (ok && n > 0) {
       const int jl = n - 1;

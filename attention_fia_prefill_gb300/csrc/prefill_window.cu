@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
         tc_fence_before();
         warp_arrive(&bar->p_full[t][c & 1]);
       }
+      if (!ok) tmem_wait_st();   // no store to TMEM is pending when it goes
       // ---------------------------------------------------------- output
       const int n_all = max(it.n_a, it.n_b);
       if (ok && n > 0) {

@@ -401,6 +401,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
       tc_fence_before();
       warp_arrive(&bar->p_full[i & 1]);
     }
+    if (!ok) tmem_wait_st();   // no store to TMEM is pending when it goes
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, wait(&bar->v_free[(n - 1) % ST], ((n - 1) / ST) & 1, abort_flag, w.limit_ns));
     tc_fence_after();
