@@ -694,7 +694,6 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       m = m_use;
     }
     if (MODE == kMask) cp_async_wait_all();   // no copy into the slot outlives the loop
-    if (!ok) tmem_wait_st();                  // no store to TMEM is pending when it goes
     // ------------------------------------------------------------ epilogue
     if (ok && n > 0) {
       const int jl = n - 1;
@@ -764,6 +763,12 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {
+    // (a warp that gave up between its stores to TMEM and the wait for them)
+    tmem_wait_st();
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
