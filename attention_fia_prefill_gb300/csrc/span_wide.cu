@@ -441,7 +441,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) span_wide_kernel(const __grid
   if (*abort_flag != 0) {
     const float nan = __uint_as_float(0x7fc00000u);
     for (int e = threadIdx.x; e < 128; e += kWideThreads) ml[e] = make_float2(nan, nan);
-    if (threadIdx.x == 0) status_raise(p.status, 10u /* FIA_ERR_TIMEOUT */);
+    if (threadIdx.x == 0) {
+      // (the word may hold anything until it has this call's epoch: a larger one
+      // would hide the raise, and the stamp below would then clear it)
+      if (p.n_parts == 0) status_stamp(p.status);
+      status_raise(p.status, 10u /* FIA_ERR_TIMEOUT */);
+    }
   }
   span_join<D, BF16, R, C::kGroups, kWideThreads>(p, reinterpret_cast<const float*>(smem + C::kOffO), ml,
                                                   smem + C::kOffIn, lg, rank, b, kvh);

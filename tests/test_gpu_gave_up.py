@@ -91,3 +91,56 @@ def test_calls_behind_ones_that_gave_up(fia):
             torch.cuda.synchronize()
             for m, g in got.items():
                 assert torch.equal(g, want[m]), (n, m)
+
+
+def outcomes(call, want, tries=30):
+    """(out, status) of short-limit calls, each on a workspace that no call has seen: `call` takes it.  The last call is
+    a good one on the last workspace."""
+    import attention_fia_prefill_gb300 as fia
+    for fill in (0, 255):
+        for _ in range(tries):
+            ws = torch.full((1 << 24,), fill, dtype=torch.uint8, device=DEV)
+            with short_waits():
+                out = call(ws)
+            yield out, fia.fia_device_status(ws)
+        assert torch.equal(call(ws), want) and fia.fia_device_status(ws) == 0
+
+
+def rows_right_or_nan(out, want):
+    """Rows that are NaN (the others have to be right)."""
+    o, w = out.reshape(-1, out.shape[-1]), want.reshape(-1, out.shape[-1])
+    gone = o.isnan().any(1)
+    assert o[gone].isnan().all() and torch.equal(o[~gone], w[~gone])
+    return int(gone.sum())
+
+
+@pytest.mark.parametrize("n1,B", [(64, 8), (24, 20), (40, 3)])
+def test_prefix_by_every_sequence_raises_its_status(fia, n1, B):
+    """Units of 17..64 rows on a workspace whose status word holds anything: rows that are NaN go with FIA_ERR_TIMEOUT."""
+    args, kw = prefix_args(n1, 1, B, 256, 2100)
+    lib = _binding.load_library()
+    lib.fia_debug_set_prefix_path(2)
+    try:
+        want = fia.fia_decode_shared_prefix(*args, **kw)[0]
+        gave_up = 0
+        for out, status in outcomes(lambda ws: fia.fia_decode_shared_prefix(*args, workspace=ws, **kw)[0], want):
+            n = rows_right_or_nan(out, want)
+            gave_up += n > 0
+            assert status == (10 if n else 0)
+    finally:
+        lib.fia_debug_set_prefix_path(0)
+    assert gave_up > 0
+
+
+def test_wide_window_decode_that_gives_up_leaves_nan(fia):
+    """No workspace: NaN in the unit's rows, the others right."""
+    q, k, v = dense(64, 1, 1, 3000, 149, B=40)
+    kw = dict(num_heads=64, num_key_value_heads=1, scale_value=0.1, input_layout="BNSD")
+    want = fia.fia_decode_window(q, k, v, **kw)[0]
+    gave_up = 0
+    for _ in range(30):
+        with short_waits():
+            out = fia.fia_decode_window(q, k, v, **kw)[0]
+        gave_up += rows_right_or_nan(out, want) > 0
+    assert gave_up > 0
+    assert torch.equal(fia.fia_decode_window(q, k, v, **kw)[0], want)
