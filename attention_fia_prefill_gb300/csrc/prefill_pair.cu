@@ -703,13 +703,16 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       tc_fence_after();
     }
     if (MODE == kPrefix) {
-      // a warp of live rows: O as it is, with its max and sum
-      if (ok && warp_rows) {
+      // a warp of live rows: O as it is, with its max and sum; after an abort NaN,
+      // which the join carries into the rows (it runs whatever happened here)
+      if (warp_rows) {
         const int64_t row = (int64_t(pb) * p.num_heads + kvh * p.group + ph) * p.q_tokens + pt + it.cost * p.part_rows;
         const bool live = pb < p.n_batch;
-        if (live) p.part_ml[row] = make_float2(m, l);
+        const float nan = __uint_as_float(0x7fc00000u);
+        if (live) p.part_ml[row] = ok ? make_float2(m, l) : make_float2(nan, nan);
 #pragma unroll
         for (int c = 0; c < DV / 32; ++c) {
+          if (!ok) break;
           uint32_t u[32];
           tmem_ld32(tmem + lane_off + col_o + c * 32, u);
           tmem_wait_ld(u);

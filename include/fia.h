@@ -455,7 +455,9 @@ FIA_API fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor*
  *          of every row of block_table must be the same; the first row's are
  *          read.  A sequence shorter than the prefix sees its own length's keys
  *          of it (values of the others must be finite).
- *   Workspace: the status word and the prefix's partial results.
+ *   Workspace: the status word and the prefix's partial results.  A bounded
+ *          wait that runs out leaves NaN in the rows it held up (and
+ *          FIA_ERR_TIMEOUT in the word).
  * ------------------------------------------------------------------------ */
 FIA_API fia_status fia_decode_shared_prefix_get_workspace_size(const fia_tensor* query, const fia_tensor* key_cache,
                                                        const fia_tensor* value_cache, const fia_tensor* block_table,

@@ -144,3 +144,21 @@ def test_wide_window_decode_that_gives_up_leaves_nan(fia):
         gave_up += rows_right_or_nan(out, want) > 0
     assert gave_up > 0
     assert torch.equal(fia.fia_decode_window(q, k, v, **kw)[0], want)
+
+
+@pytest.mark.parametrize("n1,n2,B,P", [(16, 2, 40, 1024), (4, 4, 300, 512), (64, 2, 9, 2048)])
+def test_prefix_kernel_that_gives_up_leaves_nan(fia, n1, n2, B, P):
+    """A prefix whose kernel gave up is not joined as whatever its workspace held: the rows are NaN, the status says so."""
+    args, kw = prefix_args(n1, n2, B, P, 90)
+    lib = _binding.load_library()
+    lib.fia_debug_set_prefix_path(1)
+    try:
+        want = fia.fia_decode_shared_prefix(*args, **kw)[0]
+        gave_up = 0
+        for out, status in outcomes(lambda ws: fia.fia_decode_shared_prefix(*args, workspace=ws, **kw)[0], want):
+            n = rows_right_or_nan(out, want)
+            gave_up += n > 0
+            assert status in (0, 10) and (n == 0 or status == 10)
+    finally:
+        lib.fia_debug_set_prefix_path(0)
+    assert gave_up > 0
