@@ -117,10 +117,10 @@ struct PrefillParams {
   const int32_t* kv_lens;
   int n_batch, s1, s2;            // s1 / s2: rows a batch has (TND: all rows)
   // kPrefix: tm_q is a 5-D map (D, heads of a group, q_tokens, KV_N, B) whose
-  // box holds the rows of tile_batches sequences; kv_lens the whole lengths;
-  // the prefix's s2 keys lie in the blocks of block_table's first row.
-  // Partial results as SpanParams takes them.
-  int q_tokens, tile_batches, n_pairs, n_splits;
+  // box holds the rows of tile_batches sequences; kv_lens the whole lengths,
+  // clamped to [0, kv_max]; the prefix's s2 keys lie in the blocks of
+  // block_table's first row.  Partial results as SpanParams takes them.
+  int q_tokens, tile_batches, n_pairs, n_splits, kv_max;
   int box_rows;                   // min(block_size, 128)
   float* part_o;
   float2* part_ml;

@@ -584,6 +584,7 @@ fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* k
   pp.kv_lens = p.kv_len;
   pp.n_batch = p.B;
   pp.s2 = int(shared_prefix_len);
+  pp.kv_max = p.kv_max;
   pp.q_tokens = p.q_tokens;
   pp.tile_batches = w.tile_batches;
   pp.n_pairs = w.n_pairs;

@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       pb = r < p.tile_batches * unit_rows ? (2 * it.q_tile + t) * p.tile_batches + r / unit_rows : p.n_batch;
       pt = (r % unit_rows) / p.group;
       ph = r % p.group;
-      if (pb < p.n_batch) p_end = min(max(max(p.kv_lens[pb], 0) - p.q_tokens + pt + 1, 0), p.s2);
+      if (pb < p.n_batch) p_end = min(max(min(max(p.kv_lens[pb], 0), p.kv_max) - p.q_tokens + pt + 1, 0), p.s2);
     }
     const bool warp_rows = MODE != kPrefix || __any_sync(0xffffffffu, pb < p.n_batch);
     float m = -INFINITY, l = 0.f;
