@@ -58,7 +58,8 @@ struct SpanParams {
   float scale_log2;
   DevStatus status;               // word nullable; stamped where n_parts is 0
   // partial results to join (the shared prefix): O (not divided by its sum)
-  // [n_parts][B * N1 * q_tokens][D], (max in log2 units, sum) likewise, row
+  // [n_parts][B * N1 * q_tokens][D], (max in log2 units, sum) likewise (-inf: no
+  // keys; NaN, NaN: a NaN score, or a kernel that gave up), row
   // (b * N1 + head) * q_tokens + token
   const float* part_o;
   const float2* part_ml;

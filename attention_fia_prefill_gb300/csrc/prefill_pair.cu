@@ -708,8 +708,10 @@ __global__ void __launch_bounds__(320, 1) prefill_pair_kernel(const __grid_const
       if (warp_rows) {
         const int64_t row = (int64_t(pb) * p.num_heads + kvh * p.group + ph) * p.q_tokens + pt + it.cost * p.part_rows;
         const bool live = pb < p.n_batch;
+        // (a maximum passes NaN scores over: a row with no others has -inf, which
+        // the join would take for a row without keys, and a sum that is NaN)
         const float nan = __uint_as_float(0x7fc00000u);
-        if (live) p.part_ml[row] = ok ? make_float2(m, l) : make_float2(nan, nan);
+        if (live) p.part_ml[row] = ok && l == l ? make_float2(m, l) : make_float2(nan, nan);
 #pragma unroll
         for (int c = 0; c < DV / 32; ++c) {
           if (!ok) break;

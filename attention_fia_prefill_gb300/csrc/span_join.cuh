@@ -145,7 +145,9 @@ __device__ __forceinline__ void span_join(const SpanParams& p, const float* ob, 
       a.x *= keep; a.y *= keep; a.z *= keep; a.w *= keep;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (w2[k].x == -INFINITY) continue;   // an empty part: its O may be 0 * NaN
+        // an empty part: its O may be 0 * NaN.  (Tested by its sum, so that the prefix
+        // kernel need not mark sums that are NaN: 12.0 -> 13.1 us, 64 sequences 67.7 -> 72.2.)
+        if (w2[k].x == -INFINITY) continue;
         const float w = join_weight(w2[k].x, t);
         l += w * w2[k].y;
         a.x += w * x[k].x; a.y += w * x[k].y; a.z += w * x[k].z; a.w += w * x[k].w;

@@ -54,3 +54,58 @@ def test_prefix_lengths_past_the_tables(fia, path, Q, n1, n2):
     out, lse = run(fia, q, k, v, table, lens, P, n2)
     rows = [tuple(po.cache_rows(f64(x), table[b], n, n2) for x in (k, v)) for b, n in enumerate(taken)]
     po.assert_close(out, lse, po.decode(q, rows, taken, 1 << 40, 0, 0.09))
+
+
+# ------------------------------------------------------------------ NaN scores
+@pytest.mark.parametrize("n1", [4, 20, 64])
+def test_nan_query_behind_a_prefix(fia, path, n1):
+    """A query that is NaN gives NaN, also where the sequence has no key but the prefix's; its neighbours are as ever."""
+    P, lens = 512, [512, 300, 700, 520, 0]
+    q, k, v, table = batch(n1, 1, len(lens), P, 256, workload=162 + n1)
+    want, want_l = run(fia, q, k, v, table, lens, P, 1)
+    q[:3, 1] = float("nan")
+    q[4, 1] = float("nan")     # (no keys: zeros and +inf whatever the query)
+    out, lse = run(fia, q, k, v, table, lens, P, 1)
+    assert out[:3, 1].isnan().all() and lse[:3, 1].isnan().all()
+    others = [h for h in range(n1) if h != 1]
+    assert torch.equal(out[:, others], want[:, others]) and torch.equal(lse[:, others], want_l[:, others])
+    assert torch.equal(out[3:], want[3:]) and torch.equal(lse[3:], want_l[3:])
+
+
+@pytest.mark.parametrize("n1", [4, 64])
+@pytest.mark.parametrize("tiles", [range(8), [0], [7], [2, 3]])
+def test_nan_keys_of_a_prefix(fia, path, n1, tiles):
+    """Keys of the prefix that are NaN, whole 128-key tiles of it: NaN for every sequence that sees one."""
+    P, lens = 1024, [1024, 1100, 1279, 1025]
+    q, k, v, table = batch(n1, 1, len(lens), P, 256, bs=128, workload=164 + n1)
+    k[list(tiles)] = float("nan")
+    out, lse = run(fia, q, k, v, table, lens, P, 1)
+    assert out.isnan().all() and lse.isnan().all()
+
+
+# ------------------------------------------------------------------ block ids outside the pool
+@pytest.mark.parametrize("n1", [4, 40])
+def test_ids_outside_the_pool_read_as_zeros(fia, path, n1):
+    """Negative ids and ids past the pool, in the prefix and behind it: what a block of zeros gives."""
+    P, lens = 512, [512, 640, 700, 515]
+    q, k, v, table = batch(n1, 1, len(lens), P, 256, workload=166 + n1)
+    n = k.shape[0]
+    k, v = (torch.cat([x, torch.zeros(1, *x.shape[1:], dtype=x.dtype)]) for x in (k, v))
+    table[:, 2] = table[1, 9] = table[2, 8] = n
+    want = run(fia, q, k, v, table, lens, P, 1)
+    table[:, 2], table[1, 9], table[2, 8] = -1, 2 ** 31 - 1, -2 ** 31
+    got = run(fia, q, k[:n], v[:n], table, lens, P, 1)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("kv", ["BNBD", "BSH"])
+def test_prefill_ids_outside_the_pool_read_as_zeros(fia, kv):
+    q = fia_inputs.normal((2, 4, 150, 64), "bf16", 167, 1).to(DEV)
+    shape = (5, 2, 128, 64) if kv == "BNBD" else (5, 128, 128)
+    k, v = (fia_inputs.normal(shape, "bf16", 167, i).to(DEV) for i in (2, 3))
+    k[4] = v[4] = 0
+    kw = dict(block_size=128, actual_seq_kvlen=i32([500, 300]), num_heads=4, num_key_value_heads=2, input_layout="BNSD",
+              softmax_lse_flag=True, pre_tokens=200, sink_tokens=5)
+    want = fia.fia_prefill_window(q, k, v, block_table=i32([[0, 4, 2, 4], [4, 1, 3, 0]]), **kw)
+    got = fia.fia_prefill_window(q, k[:4], v[:4], block_table=i32([[0, -1, 2, 2 ** 31 - 1], [-2 ** 31, 1, 3, 0]]), **kw)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
