@@ -116,6 +116,7 @@ struct PrefillParams {
   const int32_t* q_lens;
   const int32_t* kv_lens;
   int n_batch, s1, s2;            // s1 / s2: rows a batch has (TND: all rows)
+  int n_blocks;                   // of the pool: ids from here on are read as -1, outside its map
   // kPrefix: tm_q is a 5-D map (D, heads of a group, q_tokens, KV_N, B) whose
   // box holds the rows of tile_batches sequences; kv_lens the whole lengths,
   // clamped to [0, kv_max]; the prefix's s2 keys lie in the blocks of

@@ -289,6 +289,7 @@ fia_status window_prefill(const fia_tensor* q, const fia_tensor* k, const fia_te
     p.block_table = static_cast<const int32_t*>(table->data);
     p.table_stride = table->shape[1];
     p.block_size = int(w.bs);
+    p.n_blocks = int(std::min<int64_t>(w.blocks, kMaxInt));
   }
   return FIA_OK;
 }
@@ -323,7 +324,7 @@ struct PrefixPlan {
 // three more (start, first loads, partial results).
 PrefixPlan prefix_plan(const SpanParams& p, int64_t prefix, int64_t D, int n_sm) {
   PrefixPlan w;
-  if (prefix == 0 || p.B < 2) return w;   // one sequence shares with nobody
+  if (prefix == 0 || p.B < 2 || p.n_blocks == 0) return w;   // (one sequence shares with nobody, and nothing is read)
   w.split_off = true;
   w.tile_batches = kTileM / p.rows;
   const int64_t row_tiles = (p.B + w.tile_batches - 1) / w.tile_batches;
@@ -354,7 +355,6 @@ fia_status prefix_args(const fia_tensor* q, const fia_tensor* k, const fia_tenso
   if (prefix < 0 || prefix > p.kv_max || prefix % p.block_size != 0)
     return fail(FIA_ERR_SEQLEN, "shared_prefix_len %lld: a multiple of block_size in [0, %d]", (long long)prefix, p.kv_max);
   p.pre = int(kMaxInt);
-  if (p.n_blocks == 0) p.kv_max = 0;   // an empty pool: no keys
   return FIA_OK;
 }
 
@@ -486,22 +486,21 @@ fia_status fia_prefill_window(const fia_tensor* query, const fia_tensor* key, co
   PrefillParams& p = w.p;
   const int64_t Bmap = w.layout == L_TND ? 1 : w.B;
   FIA_TRY(dense_map(&p.tm_q, query, w.layout, Bmap, w.N1, w.S1, w.D));
-  // K/V without a row: no kernel reads them, but a map wants an extent
-  fia_tensor kk = *key, vv = *value;
-  int64_t rows = w.S2, blocks = w.blocks;
   if (numel(key) == 0) {
-    kk.data = vv.data = query->data;
-    p.kv_lens = nullptr;
-    p.s2 = 0;
-    p.block_table = nullptr;
+    // K/V without a row are not read (every id of a pool without a block lies
+    // outside it), but a map wants an extent
     p.tm_k = p.tm_v = p.tm_q;
+    if (p.block_table == nullptr) {
+      p.kv_lens = nullptr;
+      p.s2 = 0;
+    }
   } else if (p.block_table != nullptr) {
     const Layout pl = w.bnbd ? L_BNSD : L_BSND;
-    FIA_TRY(dense_map(&p.tm_k, &kk, pl, blocks, w.N2, w.bs, w.D));
-    FIA_TRY(dense_map(&p.tm_v, &vv, pl, blocks, w.N2, w.bs, w.D));
+    FIA_TRY(dense_map(&p.tm_k, key, pl, w.blocks, w.N2, w.bs, w.D));
+    FIA_TRY(dense_map(&p.tm_v, value, pl, w.blocks, w.N2, w.bs, w.D));
   } else {
-    FIA_TRY(dense_map(&p.tm_k, &kk, w.layout, Bmap, w.N2, rows, w.D));
-    FIA_TRY(dense_map(&p.tm_v, &vv, w.layout, Bmap, w.N2, rows, w.D));
+    FIA_TRY(dense_map(&p.tm_k, key, w.layout, Bmap, w.N2, w.S2, w.D));
+    FIA_TRY(dense_map(&p.tm_v, value, w.layout, Bmap, w.N2, w.S2, w.D));
   }
   p.tm_qr = p.tm_q;
   p.tm_kr = p.tm_k;
@@ -545,14 +544,14 @@ fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_tensor* k
   FIA_TRY(prefix_args(query, key_cache, value_cache, block_table, actual_seq_kvlen, params, shared_prefix_len,
                       attention_out, softmax_lse, p, D));
   const int n_sm = sm_count();
-  const PrefixPlan w = prefix_plan(p, p.kv_max == 0 ? 0 : shared_prefix_len, D, n_sm);
+  const PrefixPlan w = prefix_plan(p, shared_prefix_len, D, n_sm);
   FIA_TRY(check_ws(workspace, workspace_bytes, w.bytes));
   const bool bf16 = query->dtype == FIA_DTYPE_BF16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   if (!w.split_off || !prefix_apart(p, shared_prefix_len, D)) {
     p.status = make_status(workspace);
-    p.shared = p.kv_max == 0 ? 0 : int(shared_prefix_len);
+    p.shared = int(shared_prefix_len);
     return run_profiled(p, D, bf16, n_sm, s);
   }
   PrefillParams pp;

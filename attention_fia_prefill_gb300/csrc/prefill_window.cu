@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(WinCfg<D>::kThreads, 1) prefill_window_kernel(
             if (p.block_table != nullptr) {
               const int page = key / p.block_size;
               kv_b = __ldg(p.block_table + int64_t(it.b) * p.table_stride + page);
+              if (kv_b >= p.n_blocks) kv_b = -1;
               kv_r = key - page * p.block_size;
             }
             // K and V of the step; ahead of step 0's, Q of tile A and of tile B

@@ -383,7 +383,8 @@ FIA_API fia_status fia_cache_write(const fia_tensor* key, int64_t key_token_stri
  *   query, attention_out, softmax_lse: as fia_decode (BNSD / BSND / BSH, Q_S
  *          1..16, Q_N / KV_N * Q_S <= 64, D 64 or 128).
  *   key/value, contiguous or paged: as fia_decode (block_size a multiple of
- *          16).  Block ids outside the pool read as zeros; entries of blocks
+ *          16).  Block ids outside the pool read as zeros (of a pool without a
+ *          block every id does, here and in the two entries below); entries of blocks
  *          that no token sees are never read, so blocks behind the window may
  *          be freed.  At most 2^30 keys per sequence.
  *   actual_seq_kvlen: device int32 (B), the length L with the new tokens,

@@ -1,4 +1,7 @@
 """Edges of the paged-serving operators, the shared prefix on both of its paths."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -109,3 +112,39 @@ def test_prefill_ids_outside_the_pool_read_as_zeros(fia, kv):
     want = fia.fia_prefill_window(q, k, v, block_table=i32([[0, 4, 2, 4], [4, 1, 3, 0]]), **kw)
     got = fia.fia_prefill_window(q, k[:4], v[:4], block_table=i32([[0, -1, 2, 2 ** 31 - 1], [-2 ** 31, 1, 3, 0]]), **kw)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# ------------------------------------------------------------------ pools without a block
+@pytest.mark.parametrize("n1", [4, 40])
+@pytest.mark.parametrize("P", [0, 64])
+def test_prefix_empty_pool_reads_as_zeros(fia, path, n1, P):
+    """As fia_decode_window: every key and value of a length is 0, so out = 0 and lse = log(keys seen)."""
+    lens = [100, 0, 64, 1, 10 ** 6]
+    q, _, _, _ = batch(n1, 1, len(lens), 0, 0, Q=1, workload=168)
+    pool = torch.zeros(0, 1, 32, 128, dtype=torch.bfloat16)
+    table = torch.zeros(len(lens), 4, dtype=torch.int32)
+    out, lse = run(fia, q, pool, pool, table, lens, P, 1)
+    o2, l2 = fia.fia_decode_window(q.to(DEV), pool.to(DEV), pool.to(DEV), block_table=table.to(DEV), block_size=32,
+                                   actual_seq_kvlen=i32(lens), num_heads=n1, num_key_value_heads=1, scale_value=0.09,
+                                   input_layout="BNSD", softmax_lse_flag=True)
+    seen = torch.tensor([math.log(n) if n else math.inf for n in (100, 0, 64, 1, 128)]).view(-1, 1, 1, 1)
+    for o, l in ((out, lse), (o2, l2)):
+        assert (o == 0).all() and torch.isposinf(l[1]).all()
+        live = [0, 2, 3, 4]
+        # log2 of a sum of at most 128 ones and its product with ln 2, in fp32: 1e-5 is over ten steps of either
+        assert (l.cpu()[live] - seen[live]).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("kv", ["BNBD", "BSH"])
+def test_prefill_empty_pool_reads_as_zeros(fia, kv):
+    """Rows that see keys give 0 and log(keys seen), rows that see none 0 and +inf."""
+    q = fia_inputs.normal((3, 2, 300, 64), "bf16", 169, 1).to(DEV)
+    pool = torch.zeros((0, 1, 128, 64) if kv == "BNBD" else (0, 128, 64), dtype=torch.bfloat16, device=DEV)
+    lens, pre, sink = [300, 500, 0], 99, 3
+    out, lse = fia.fia_prefill_window(q, pool, pool, block_table=torch.zeros(3, 4, dtype=torch.int32, device=DEV), block_size=128,
+                                      actual_seq_kvlen=i32(lens), num_heads=2, num_key_value_heads=1, input_layout="BNSD",
+                                      softmax_lse_flag=True, pre_tokens=pre, sink_tokens=sink)
+    assert (out == 0).all() and torch.isposinf(lse[2]).all()
+    for b in (0, 1):
+        n = po.window_see(300, lens[b], pre, sink).sum(1)
+        assert np.abs(lse[b, :, :, 0].cpu().double().numpy() - np.log(n)).max() < 1e-5
