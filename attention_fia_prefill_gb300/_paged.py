@@ -16,6 +16,7 @@ import importlib.machinery
 import importlib.util
 import os
 
+from . import build
 from ._binding import INT32_MAX, LIB_PATH, FIAError
 
 EXT_PATH = os.path.join(os.path.dirname(LIB_PATH), "_fia_paged.so")
@@ -26,7 +27,10 @@ def _load():
     global _ext
     if not os.path.exists(EXT_PATH):
         raise ImportError(f"{os.path.basename(EXT_PATH)} not built at {EXT_PATH}; run attention_fia_prefill_gb300.build.build()")
-    import torch  # noqa: F401  (its libraries are what the binding links to)
+    import torch   # (its libraries are what the binding links to)
+    if build.ext_torch_version() != torch.__version__:
+        raise ImportError(f"{os.path.basename(EXT_PATH)} was built against torch {build.ext_torch_version() or '?'}, this is "
+                          f"{torch.__version__}; run attention_fia_prefill_gb300.build.build()")
     loader = importlib.machinery.ExtensionFileLoader("_fia_paged", EXT_PATH)
     ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fia_paged", loader))
     loader.exec_module(ext)

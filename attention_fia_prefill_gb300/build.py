@@ -3,14 +3,17 @@ compiled Python binding of the paged-serving operators on top of it.
 
 Each translation unit compiles in parallel; the .cu objects link into one
 shared library next to this file (_lib/libfia.so), the binding into
-_lib/_fia_paged.so, which needs libfia.so and the installed torch.  Rebuilds
-only when a source or header is newer than the libraries.
+_lib/_fia_paged.so, which needs libfia.so and the installed torch (where there
+is none, libfia.so alone is built: its callers need the CUDA toolkit only).
+Rebuilds only what is older than its sources and headers, and a binding built
+against another torch.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -21,6 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libfia.so")
 EXT = os.path.join(OUT_DIR, "_fia_paged.so")
+EXT_TORCH = os.path.join(OUT_DIR, "_fia_paged.torch")   # the torch that the binding was built against
 EXT_SOURCE = os.path.join(CSRC, "py_paged.cpp")
 SOURCES = ["fia_api.cu", "prefill.cu", "prefill_pair.cu", "bsa_fp8.cu", "decode.cu", "decode_d64.cu", "decode_gqa.cu", "decode_noalloc.cu",
            "mla.cu", "paged_api.cu", "paged.cu", "span_decode.cu", "span_wide.cu", "prefill_window.cu"]
@@ -43,18 +47,48 @@ def _inputs():
     return files, headers
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
-        return False
+def _torch():
+    """(folder, version) of the installed torch with CUDA, located without importing it, or None."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    where = spec.submodule_search_locations[0]
+    if not os.path.exists(os.path.join(where, "lib", "libtorch_cuda.so")):
+        return None
+    with open(os.path.join(where, "version.py")) as f:
+        return where, re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M).group(1)
+
+
+def _newer(target, files) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in files)
+
+
+def _lib_current() -> bool:
     files, headers = _inputs()
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return all(os.path.getmtime(f) <= t for f in files + headers + [EXT_SOURCE, os.path.abspath(__file__)])
+    return _newer(LIB, files + headers + [os.path.abspath(__file__)])
 
 
-def _ext_commands(cc):
-    """(compile, link) commands of the binding: host code against the headers of torch (located without importing
-    it), Python and the CUDA toolkit."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def ext_torch_version() -> str:
+    """Version of the torch that the binding was built against ("": no binding)."""
+    if not os.path.exists(EXT) or not os.path.exists(EXT_TORCH):
+        return ""
+    with open(EXT_TORCH) as f:
+        return f.read().strip()
+
+
+def _ext_current(torch) -> bool:
+    headers = [os.path.join(ROOT, "include", "fia.h")]
+    return ext_torch_version() == torch[1] and _newer(EXT, headers + [EXT_SOURCE, os.path.abspath(__file__)])
+
+
+def up_to_date() -> bool:
+    torch = _torch()
+    return _lib_current() and (torch is None or _ext_current(torch))
+
+
+def _ext_commands(cc, torch):
+    """(compile, link) commands of the binding: host code against the headers of torch (its folder), Python and the
+    CUDA toolkit."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(cc)))
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
@@ -75,7 +109,12 @@ def _run(cmd, what, verbose=False):
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
-    if not force and up_to_date():
+    torch = _torch()
+    want_lib = force or not _lib_current()
+    want_ext = torch is not None and (force or not _ext_current(torch))
+    if torch is None and verbose:
+        print("no torch with CUDA here: libfia.so is built without the Python binding of the paged-serving operators")
+    if not want_lib and not want_ext:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     files, _ = _inputs()
@@ -88,16 +127,22 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         _run(cmd, f"nvcc for {src}", verbose)
         return obj
 
-    ext_compile, ext_link = _ext_commands(cc)
     with cf.ThreadPoolExecutor(max_workers=len(files) + 1) as ex:
-        ext = ex.submit(_run, ext_compile, f"compiling {EXT_SOURCE}", verbose)
-        objs = list(ex.map(compile_one, files))
-        ext.result()
-    tmp = LIB + ".tmp"
-    _run([cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs], "link")
-    os.replace(tmp, LIB)
-    _run(ext_link, "binding link")
-    os.replace(EXT + ".tmp", EXT)
+        if want_ext:
+            ext_compile, ext_link = _ext_commands(cc, torch[0])
+            ext = ex.submit(_run, ext_compile, f"compiling {EXT_SOURCE}", verbose)
+        if want_lib:
+            tmp = LIB + ".tmp"
+            _run([cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *ex.map(compile_one, files)], "link")
+            os.replace(tmp, LIB)
+        if want_ext:
+            ext.result()
+            _run(ext_link, "binding link")
+            if os.path.exists(EXT_TORCH):
+                os.remove(EXT_TORCH)
+            os.replace(EXT + ".tmp", EXT)
+            with open(EXT_TORCH, "w") as f:
+                f.write(torch[1] + "\n")
     return LIB
 
 
