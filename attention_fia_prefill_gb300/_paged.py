@@ -45,10 +45,11 @@ def fia_block_table_append(context_lens, new_lens, free_blocks, block_table, *, 
     token to its slot of the paged cache.
 
     context_lens, new_lens: int32 (B), tokens held and to append; free_blocks:
-    int32 (F), ids handed out from the front; block_table: int32 (B, W), changed
-    in place; num_tokens: slots to write, at least the sum of new_lens.  Returns
-    (slot_mapping (num_tokens), kv_lens (B), cu_new_lens (B), num_blocks (1)),
-    all int32; num_blocks above F says that the list ran out."""
+    int32 (F), ids handed out from the front (the list stays as it is: the next
+    call takes it without its first num_blocks ids); block_table: int32 (B, W),
+    changed in place; num_tokens: slots to write, at least the sum of new_lens.
+    Returns (slot_mapping (num_tokens), kv_lens (B), cu_new_lens (B), num_blocks
+    (1)), all int32; num_blocks above F says that the list ran out."""
     return (_ext or _load()).block_table_append(context_lens, new_lens, free_blocks, block_table, block_size, num_tokens,
                                                 slot_mapping, kv_lens, cu_new_lens, num_blocks)
 

@@ -336,6 +336,8 @@ FIA_API fia_status bsa_forward_fp8(const fia_tensor* query, const fia_tensor* ke
  *          tokens to append (negative: 0).  Request b holds ceil(context /
  *          block_size) blocks and needs ceil((context + new) / block_size).
  *   free_blocks: int32 (F), ids handed out from the front, in request order.
+ *          The list is not changed: the next call takes it without its first
+ *          min(num_blocks, F) ids, or it hands the same blocks out again.
  *   block_table: int32 (B, W), in place: the columns of the blocks that a
  *          request lacked are written, every other entry stays as it was.
  *   slot_mapping: int32 (T), out: slot block_id * block_size + offset of every
@@ -473,7 +475,9 @@ FIA_API fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_t
                                     void* stream);
 
 /* Waits for `stream`, then returns the device-side status recorded in a
- * workspace by the last call that used it (FIA_OK or FIA_ERR_TIMEOUT). */
+ * workspace by the last call that used it (FIA_OK or FIA_ERR_TIMEOUT).  The
+ * replays of a captured call are one call here: a timeout of one is reported
+ * until another call uses the workspace. */
 FIA_API fia_status fia_device_status(const void* workspace, void* stream);
 
 /* Static description of a status code. */

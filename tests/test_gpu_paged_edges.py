@@ -148,3 +148,21 @@ def test_prefill_empty_pool_reads_as_zeros(fia, kv):
     for b in (0, 1):
         n = po.window_see(300, lens[b], pre, sink).sum(1)
         assert np.abs(lse[b, :, :, 0].cpu().double().numpy() - np.log(n)).max() < 1e-5
+
+
+# ------------------------------------------------------------------ the free list from step to step
+def test_no_block_is_handed_out_twice(fia):
+    """Steps that take the free list on by what the step before asked for: every block has one owner."""
+    B, bs, r = 6, 16, np.random.default_rng(7)
+    free = torch.from_numpy(r.permutation(200).astype(np.int32)).to(DEV)
+    table = torch.full((B, 30), -1, dtype=torch.int32, device=DEV)
+    ctx, held = i32([0] * B), 0
+    for _ in range(12):
+        new = [int(x) for x in r.integers(0, 40, B)]
+        slots, kv, _, used = fia.fia_block_table_append(ctx, i32(new), free, table, block_size=bs, num_tokens=sum(new))
+        free = free[int(used):]
+        ctx.copy_(kv)
+        held += int(used)
+        owned = table[table >= 0]
+        assert len(owned) == held == sum(-(-n // bs) for n in ctx.tolist()) and len(set(owned.tolist())) == held
+        assert len(set(slots.tolist())) == sum(new) and int(slots.min()) >= 0
