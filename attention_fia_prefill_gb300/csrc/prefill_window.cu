@@ -28,8 +28,8 @@
 //     (setmaxnreg; 384 threads x 168 = 128 x 120 + 256 x 192): a few spilled ones
 //     in the softmax's loop cost 5%, 294 -> 275 us with a path of their own for
 //     edge tiles; without that path 258.
-// Ragged prompts (8 sequences of 256..4096, 32 heads, window 1024): 258 us, one
-// CTA per item 350; chunks of 2048 after contexts up to 14336, window 4096: 726
+// Ragged prompts (8 sequences of 256..4096, 32 heads, window 1024): 253 us, one
+// CTA per item 350; chunks of 2048 after contexts up to 14336, window 4096: 720
 // and 837 us.  Bound: the chain of a tile's step (products 1024 cycles, softmax
 // 1300, hand-over 600) with two tiles in flight, and an item's first and last
 // steps and output, about 4 us.
