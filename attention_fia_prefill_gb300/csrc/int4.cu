@@ -47,7 +47,8 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // (16-byte loads) and writes the D/8 bytes of units (D/32) 2t .. (one store).
 // Steps and codes are the format's to the last bit, in fp32:
 //   * step: the least value of the type that is, times 15 (exact in fp32), not below
-//     the difference; that is rounded up, which changes no such comparison.
+//     the difference; that is rounded up, which changes no such comparison.  In f16 the
+//     value before it, where 15 of it would pass 65504 - low.
 //   * code: c = round((x - low) / step (1 - 2^-20)), by one addition and one fused
 //     multiply-add into 1.5 * 2^23, whose low bits then hold it.  The factor takes
 //     off more than the roundings can add, so c is the code or one less; it is one
@@ -107,6 +108,8 @@ __global__ void __launch_bounds__(kInt4Threads) cache_write_int4_kernel(const __
     const float near = fmaxf(range * ((1.f - 0x1p-21f) / 15.f), kInt4Tiny<BF16>);
     uint32_t bits = BF16 ? bf16_bits(near) : half_bits(near);
     bits += 15.f * int4_pair<BF16>(bits).x < range ? 1u : 0u;
+    // (15 steps are a number of fp32, so the comparison with what the rounding down leaves is that with 65504 - low)
+    if constexpr (!BF16) bits -= range > 0.f && 15.f * int4_pair<BF16>(bits).x > __fsub_rd(kInt4MostHalf, low) ? 1u : 0u;
     word[k] = bits | ((fine ? lo[k] & 0xffffu : 0x7fffu) << 16);
     const float step = int4_pair<BF16>(bits).x, inv = rcp_approx(step) * (1.f - 0x1p-20f), mid = 0.5f * step;
     constexpr float kMagic = 12582912.f;   // 0x4B400000: its low bits are the rounded sum's

@@ -329,8 +329,8 @@ __device__ __forceinline__ void join_unit(const SpanParams& p, const float* ob, 
     const bool has = l != 0.f;   // a NaN sum stays a NaN
     const float inv = has ? 1.f / l : 0.f;
     uint2 u;
-    u.x = has ? pack2(a.x * inv, a.y * inv, BF16) : 0u;
-    u.y = has ? pack2(a.z * inv, a.w * inv, BF16) : 0u;
+    u.x = has ? int4_out<BF16>(a.x * inv, a.y * inv) : 0u;
+    u.y = has ? int4_out<BF16>(a.z * inv, a.w * inv) : 0u;
     T* orow = static_cast<T*>(p.out) + int64_t(b) * p.q_sb + int64_t(head) * p.q_sn + int64_t(tokn) * p.q_ss;
     *reinterpret_cast<uint2*>(orow + c4 * 4) = u;
     if (p.lse != nullptr && c4 == 0)
@@ -1004,8 +1004,8 @@ __global__ void __launch_bounds__(256) int4_join_kernel(const __grid_constant__ 
     const bool has = l != 0.f;   // a NaN sum stays a NaN
     const float inv = has ? 1.f / l : 0.f;
     uint2 u;
-    u.x = has ? pack2(a.x * inv, a.y * inv, BF16) : 0u;
-    u.y = has ? pack2(a.z * inv, a.w * inv, BF16) : 0u;
+    u.x = has ? int4_out<BF16>(a.x * inv, a.y * inv) : 0u;
+    u.y = has ? int4_out<BF16>(a.z * inv, a.w * inv) : 0u;
     T* orow = static_cast<T*>(p.out) + int64_t(head.x) * p.q_sb + int64_t(n1) * p.q_sn + int64_t(tok) * p.q_ss;
     *reinterpret_cast<uint2*>(orow + c4 * 4) = u;
     if (p.lse != nullptr && c4 == 0)

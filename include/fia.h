@@ -482,7 +482,8 @@ FIA_API fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_t
  * 0..15 for each value, which stands for low + step * code:
  *     low  = min x
  *     step = max((max x - min x) / 15, tiny), rounded up to t;  tiny = 2^-60
- *            (bf16) or 2^-24 (f16)
+ *            (bf16) or 2^-24 (f16).  f16: rounded down where low + 15 step
+ *            would be above 65504 and max x above min x
  *     code = ceil((x - low) / step - 1/2): the nearest one, and the lower of
  *            two equally near
  *   A group that holds a NaN, an infinity or a value beyond 2^60 in magnitude

@@ -1,0 +1,93 @@
+"""Edges of the 4-bit cache on the GPU: values at the top of f16, factors of the scores at the ends of fp32, keys that a
+token does not see with steps far above the others', and windows on evenly shared work."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int4_oracle as io
+from oracle.fia_oracle import f64
+
+from .test_gpu_int4 import DEV, DTYPES, i32, pools, slot_rows
+
+pytestmark = pytest.mark.gpu
+SHARED = 1 << 20     # keys of the tables' room that make a call of two units or more one of much work
+
+
+def written(fia, k, v, G, bs=16, layout="BNBD", dt="bf16"):
+    """Keys and values (B, L, N, D) -> pools and the tables of a sequence's own blocks."""
+    B, L, n2, D = k.shape
+    W = -(-L // bs)
+    p = pools(B * W, n2, bs, D, G, layout, dt)
+    slots = (torch.arange(B)[:, None] * (W * bs) + torch.arange(L)).reshape(-1)
+    fia.fia_cache_write_int4(k.reshape(-1, n2, D).to(DTYPES[dt]).to(DEV), v.reshape(-1, n2, D).to(DTYPES[dt]).to(DEV), *p,
+                             slots.to(torch.int32).to(DEV))
+    return p, torch.arange(B * W, dtype=torch.int32).view(B, W)
+
+
+def attend(fia, q, p, table, lens, bs=16, scale=1.0, room=0, **kw):
+    """-> out, lse and the oracle's, of BNSD queries; room: keys that the tables have room for."""
+    n1, n2 = q.shape[1], p[2].shape[1]
+    wide = torch.zeros(table.shape[0], max(table.shape[1], room // bs), dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    out, lse = fia.fia_decode_window_int4(q.to(DEV), *p, actual_seq_kvlen=i32(lens), block_table=wide.to(DEV), block_size=bs,
+                                          num_heads=n1, num_key_value_heads=n2, scale_value=scale, input_layout="BNSD",
+                                          softmax_lse_flag=True, **kw)
+    parts = [io.pool_parts(p[0], p[2]), io.pool_parts(p[1], p[3])]
+    rows = [[io.rows(x, table[b].numpy(), n) for b, n in enumerate(lens)] for x in parts]
+    return out, lse, io.decode(q, *rows, lens, kw.get("pre_tokens", 1 << 40), kw.get("sink_tokens", 0), scale)
+
+
+# ------------------------------------------------------------------ the top of f16
+def _groups_up_to(top, every):
+    """A group of 64 for every (every-th) finite f16 low up to `top`: low, top, and values between them."""
+    low = torch.arange(-32768, 32768).to(torch.int16).view(torch.float16)
+    low = low[low.isfinite() & (low <= top)][::every].double()[:, None]
+    u = torch.rand(low.shape[0], 64, generator=torch.Generator().manual_seed(int(top)), dtype=torch.float64)
+    u[:, 5], u[:, 40] = 0.0, 1.0
+    return (low + (top - low) * u).half()
+
+
+@pytest.mark.parametrize("top,every", [(65504.0, 1), (65472.0, 5), (65440.0, 5), (65408.0, 5), (65376.0, 5)])
+def test_f16_groups_at_the_top_of_the_type(fia, top, every):
+    """Finite values read back finite, half a step off at most: the step is rounded down where code 15 would otherwise
+    stand for more than the type holds."""
+    x = _groups_up_to(top, every)
+    x = torch.cat([x, x[:1].expand(-x.shape[0] % 16, -1)])[:, None]
+    T, bs = x.shape[0], 16
+    p = pools(T // bs, 1, bs, 64, 64, "BNBD", "f16")
+    fia.fia_cache_write_int4(x.to(DEV), x.to(DEV), *p, torch.arange(T, dtype=torch.int32, device=DEV))
+    k, v = fia.fia_cache_read_int4(*p, block_table=torch.arange(T // bs, dtype=torch.int32, device=DEV)[None], cu_kv_lens=i32([T]),
+                                   num_tokens=T)
+    assert k.isfinite().all() and torch.equal(k, v)
+    step = f64(p[2])[..., 0, 0].reshape(-1, 1, 1)
+    # the nearest code: what it stands for is at most |x| + step / 2 in magnitude, and is rounded to 24 bits, then to 11
+    off = np.abs(f64(k) - f64(x)) - 2.0 ** -11 * (1 + 2.0 ** -10) * (np.abs(f64(x)) + step / 2) - 2.0 ** -25
+    assert (off <= step / 2).all()
+    code, want, low = io.quantise(x, 64)
+    got_c, got_s = slot_rows(p[0], p[2])
+    assert np.array_equal(got_c, io.pack(code)) and np.array_equal(f64(got_s), np.stack([want, low], -1))
+
+
+@pytest.mark.parametrize("n1,D,G,room", [(1, 128, 32, 0), (4, 64, 32, 0), (8, 128, 128, SHARED), (16, 128, 64, 0), (32, 64, 64, 0),
+                                         (64, 128, 128, 0), (40, 64, 64, SHARED), (64, 128, 32, SHARED)])
+def test_f16_decode_at_the_top_of_the_type(fia, n1, D, G, room):
+    """Outputs that are averages of values up to the type's largest are finite, and right."""
+    B, L = 3, 90
+    g = torch.Generator().manual_seed(n1 + D)
+    k = torch.randn(B, L, 1, D, generator=g)
+    v = torch.randn(B, L, 1, D, generator=g) * 30000
+    v[..., ::4] = 65504.0
+    v[..., 1::8] = -65504.0
+    v[:, ::2, :, 2::8] = 65472.0
+    v = v.clamp(-65504, 65504)
+    p, table = written(fia, k, v, G, dt="f16")
+    q = torch.randn(B, n1, 1, D, generator=g).half()
+    q[0] = 0.0
+    for lens in ([90, 1, 2], [77, 33, 16]):
+        out, lse, ref = attend(fia, q, p, table, lens, scale=D ** -0.5, room=room)
+        assert out.isfinite().all()
+        io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D)
+    # keys as large: scores of their size, but for small queries
+    p, table = written(fia, v, k, G, dt="f16")
+    out, lse, ref = attend(fia, (q.float() * 1e-5).half(), p, table, [90, 1, 17], scale=0.125, room=room)
+    io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D)
