@@ -217,6 +217,7 @@ struct Share {
       at = from;
       end = mul_div(w, blockIdx.y + 1, g, small);
     }
+    __syncwarp();              // another lane may go on from these in next(); shuffles and votes do not order memory
     if (int(blockIdx.y) >= g) return;
     int64_t before = 0;        // of the sequences before
     for (int b0 = 0;;) {

@@ -91,3 +91,24 @@ def test_f16_decode_at_the_top_of_the_type(fia, n1, D, G, room):
     p, table = written(fia, v, k, G, dt="f16")
     out, lse, ref = attend(fia, (q.float() * 1e-5).half(), p, table, [90, 1, 17], scale=0.125, room=room)
     io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D)
+
+
+# ------------------------------------------------------------------ work shared evenly among the CTAs
+@pytest.mark.parametrize("n1,Q,D,G", [(4, 1, 128, 128), (8, 2, 64, 32), (16, 4, 64, 64), (16, 4, 128, 32)])
+def test_shares_that_begin_with_any_sequence(fia, n1, Q, D, G):
+    """Shares whose first unit any lane finds, in the first 32 sequences and behind them, with nothing else to do and with
+    much: the oracle's results, and the same bits on every run."""
+    B, L = 200, 70
+    g = torch.Generator().manual_seed(n1 + G)
+    p, table = written(fia, *(torch.randn(4, L, 1, D, generator=g) for _ in range(2)), G)
+    table = table[torch.arange(B) % 4]
+    q = torch.randn(B, n1, Q, D, generator=g).bfloat16()
+    for first, every in ((0, 1), (1, 7), (31, 33), (64, 2), (199, 1), (97, 50)):
+        lens = [L - b % 9 if b >= first and (b - first) % every == 0 else 0 for b in range(B)]
+        out, lse, ref = attend(fia, q, p, table, lens, scale=D ** -0.5, room=SHARED)
+        io.assert_close(out, lse, ref, L, wide=n1 * Q > 32 and G == D)
+        wide = torch.nn.functional.pad(table, (0, SHARED // 16 - table.shape[1])).to(DEV)
+        for _ in range(5):
+            again = fia.fia_decode_window_int4(q.to(DEV), *p, actual_seq_kvlen=i32(lens), block_table=wide, block_size=16, num_heads=n1,
+                                               num_key_value_heads=1, scale_value=D ** -0.5, input_layout="BNSD")
+            assert torch.equal(again[0], out)
