@@ -9,8 +9,8 @@
 // subnormal fp16: code 2^-24 in bits 0-3, code 2^-20 in bits 4-7 (products of
 // subnormals are exact on the tensor cores, into fp32): one AND makes two values,
 // with no conversion and nothing rounded.
-//   * Q, scaled by a power of two per row to just below 2^11 in magnitude, is
-//     fp16 (exact but for values below 2^-25 of the row's largest, off by 2^-36
+//   * Q, scaled by a power of two per row to just below 2^11 in magnitude (q_exponent),
+//     is fp16 (exact but for values below 2^-25 of the row's largest, off by 2^-36
 //     of it); what multiplies bits 0-3 is 16 times that, so that both places
 //     weigh the same.
 //   * P' = 2^(S - m) step_j is fp16 (11 bits; a bf16 P would have 8): m is the
@@ -52,6 +52,7 @@
 // behind the first).
 #pragma once
 #include <algorithm>
+#include <cfloat>
 
 #include "int4.cuh"
 #include "span_join.cuh"
@@ -137,6 +138,13 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t p_rest(uint64_t p, uint32_t rounded, uint64_t sum) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&rounded));
   return f2_fma(f2_fma(f2_pack(h.x, h.y), f2_pack(-1.f, -1.f), p), f2_pack(7.5f, 7.5f), sum);
+}
+// e with 2^10 <= top 2^-e < 2^11 for a query row of magnitude top, and so large that
+// 2^e scale is a normal number: times a hidden score, which is -inf, a factor of 0 would be a
+// NaN.  (A row that this scales below 2^10, one of zeros for one, loses digits at 2^-25 times
+// 2^e, which scores do not see: 2^e scale is 2^-120 then.)
+__device__ __forceinline__ int q_exponent(float top, float scale) {
+  return max(max(int(__float_as_uint(top) >> 23) - 137, 7 - int(__float_as_uint(scale) >> 23)), -125);
 }
 __device__ __forceinline__ float log2_approx(float x) {
   float y;
@@ -471,7 +479,8 @@ int4_decode_kernel(const __grid_constant__ Int4SpanParams ip) {
   uint32_t qb[QS ? 1 : NT][U][4];
   const uint32_t q_at = smem_u32(smem + (SPLIT ? C::kOffQShare : C::kOffQ)) + (rt * NT * U * 32 + lane) * 16;
   // of this lane's rows, as pairs: sums over a group's columns, and the factor to log2
-  // units (both in the products' units of 2^-20)
+  // units.  (The products come in units of 2^-20: f16 has both in these.  A bf16 row's
+  // factor may be so large that fp32 does not hold 2^20 of it, so K's steps get them.)
   uint64_t qs[NT][NG], cr[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -495,9 +504,7 @@ int4_decode_kernel(const __grid_constant__ Int4SpanParams ip) {
       }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^e with 2^10 <= top 2^-e < 2^11, within what a float's exponent holds (a row
-    // of zeros and one with an infinity, whose results are NaN, take the ends)
-    const int e = min(max(int(__float_as_uint(top) >> 23) - 137, -125), 125);
+    const int e = q_exponent(top, p.scale_log2);
     const float up = __uint_as_float(uint32_t(127 + e) << 23), down = __uint_as_float(uint32_t(127 - e) << 23);
     float sum[NG], c[U][8];
 #pragma unroll
@@ -526,12 +533,13 @@ int4_decode_kernel(const __grid_constant__ Int4SpanParams ip) {
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-      sum[k] = (sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 2)) * 0x1p-20f;
+      sum[k] = (sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 2)) * (BF16 ? 1.f : 0x1p-20f);
       const float s0 = __shfl_sync(0xffffffffu, sum[k], 8 * fr), s1 = __shfl_sync(0xffffffffu, sum[k], 8 * fr + 4);
       qs[nt][k] = f2_pack(s0, s1);
     }
-    const float f0 = __shfl_sync(0xffffffffu, up, 8 * fr), f1 = __shfl_sync(0xffffffffu, up, 8 * fr + 4);
-    cr[nt] = f2_pack(f0 * 0x1p20f * p.scale_log2, f1 * 0x1p20f * p.scale_log2);
+    const float f = fminf((BF16 ? up : up * 0x1p20f) * p.scale_log2, FLT_MAX);
+    const float f0 = __shfl_sync(0xffffffffu, f, 8 * fr), f1 = __shfl_sync(0xffffffffu, f, 8 * fr + 4);
+    cr[nt] = f2_pack(f0, f1);
   }
 
   const int L = min(max(len, 0), p.kv_max);
@@ -724,7 +732,9 @@ int4_decode_kernel(const __grid_constant__ Int4SpanParams ip) {
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
           const float2 g = int4_pair<BF16>(kw[q][k]);
-          const uint64_t step2 = f2_pack(g.x, g.x), low2 = f2_pack(g.y, g.y);
+          // (by the exponent: a step of 0, of a page outside the pool, meets codes of 0)
+          const float step = BF16 ? __uint_as_float((kw[q][k] << 16) + (20u << 23)) : g.x;
+          const uint64_t step2 = f2_pack(step, step), low2 = f2_pack(g.y, g.y);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float y[2];

@@ -28,6 +28,7 @@
 // K and V unpacked by four warps each were slower (184 -> 217 us), K twice and V once too
 // (174 -> 233).
 #include <algorithm>
+#include <cfloat>
 #include <cstring>
 
 #include "host.h"
@@ -213,8 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_wide_kernel(const __grid_con
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^e with 2^10 <= top 2^-e < 2^11, as in int4_decode.cuh
-    const int e = min(max(int(__float_as_uint(top) >> 23) - 137, -125), 125);
+    const int e = int4_detail::q_exponent(top, p.scale_log2);
     const float up = __uint_as_float(uint32_t(127 + e) << 23), down = __uint_as_float(uint32_t(127 - e) << 23);
     float sum = 0.f;
 #pragma unroll
@@ -228,11 +228,9 @@ __global__ void __launch_bounds__(kThreads, 2) int4_wide_kernel(const __grid_con
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     if (r < R) {
       if (t == 0) {
-        // (products come in units of 2^-20)
         float* row = reinterpret_cast<float*>(smem + C::kOffRow);
-        const float f = up * p.scale_log2;
-        row[r] = sum * 0x1p-20f;
-        row[R + r] = f * 0x1p20f;
+        row[r] = sum;
+        row[R + r] = fminf(up * p.scale_log2, FLT_MAX);
       }
 #pragma unroll
       for (int gh = 0; gh < 2; ++gh)
@@ -393,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_wide_kernel(const __grid_con
         for (int d = 1; d < 16; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
         float* f = reinterpret_cast<float*>(smem + C::kOffScale + (it & 3) * C::kScale) + dw * kTile + lane;
         if (lane < kTile) {
-          f[0] = kk.x;
+          f[0] = kk.x * 0x1p20f;   // (products come in units of 2^-20)
           f[kKeys] = kk.y;
           f[2 * kKeys] = vv.x;
           f[3 * kKeys] = vv.y;

@@ -493,8 +493,8 @@ FIA_API fia_status fia_decode_shared_prefix(const fia_tensor* query, const fia_t
  *   .. + 3, the first in its lowest four bits (g in 0..7, j in 0..D/32-1).
  *   Scales: t (blocknum, KV_N, block_size, D/G, 2), (step, low) of every group,
  *   head-major in both layouts of the codes.  Their shape says what G is.
- *   Steps must be 0 or within [2^-60, 2^60], low values a NaN or at most 2^60 in
- *   magnitude (those written are).
+ *   Steps must be within [2^-60, 2^60], or 0 with codes of 0, low values a NaN or at
+ *   most 2^60 in magnitude (those written are).
  *   Codes and scales are 16-byte aligned; keys and values agree in all this.
  *
  * fia_cache_write_int4: fia_cache_write into such a cache.
@@ -528,9 +528,10 @@ FIA_API fia_status fia_cache_read_int4(const fia_tensor* key_cache, const fia_te
  * fia_decode_window_int4: fia_decode_window over such a cache (paged only).
  * Query, lengths, window, sinks, outputs and what rows without a key give: as
  * there; scores and sums are those of the values that the codes stand for,
- * unrounded.  Block ids outside the pool read as zeros, blocks that no token
- * sees are not read, and what a key that a token does not see holds has no part
- * in that token's result.
+ * unrounded.  scale_value times a query value must be below 2^116 in magnitude
+ * (f16) or fit fp32 (bf16).  Block ids outside the pool read as zeros, blocks that
+ * no token sees are not read, and what a key that a token does not see holds has
+ * no part in that token's result.
  *   Workspace: partial results, of calls with much work; of others the size is 0
  *          and workspace may be NULL.  No status word: a bounded wait that runs out
  *          (units of more than 32 rows) leaves NaN in the rows that it held up.

@@ -25,7 +25,7 @@ def written(fia, k, v, G, bs=16, layout="BNBD", dt="bf16"):
 
 
 def attend(fia, q, p, table, lens, bs=16, scale=1.0, room=0, **kw):
-    """-> out, lse and the oracle's, of BNSD queries; room: keys that the tables have room for."""
+    """-> out, lse, the oracle's and (f16) its middles, of BNSD queries; room: keys that the tables have room for."""
     n1, n2 = q.shape[1], p[2].shape[1]
     wide = torch.zeros(table.shape[0], max(table.shape[1], room // bs), dtype=torch.int32)
     wide[:, :table.shape[1]] = table
@@ -34,7 +34,14 @@ def attend(fia, q, p, table, lens, bs=16, scale=1.0, room=0, **kw):
                                           softmax_lse_flag=True, **kw)
     parts = [io.pool_parts(p[0], p[2]), io.pool_parts(p[1], p[3])]
     rows = [[io.rows(x, table[b].numpy(), n) for b, n in enumerate(lens)] for x in parts]
-    return out, lse, io.decode(q, *rows, lens, kw.get("pre_tokens", 1 << 40), kw.get("sink_tokens", 0), scale)
+    span = kw.get("pre_tokens", 1 << 40), kw.get("sink_tokens", 0), scale
+    middle = None
+    if q.dtype == torch.float16:
+        D = q.shape[-1]
+        steps = np.repeat(f64(p[3]).transpose(0, 2, 1, 3, 4)[..., 0], D // p[3].shape[3], -1)
+        steps = [io.rows((steps,), table[b].numpy(), n)[0] for b, n in enumerate(lens)]
+        middle = io.middles(q, *rows, steps, lens, *span)
+    return out, lse, io.decode(q, *rows, lens, *span), middle
 
 
 # ------------------------------------------------------------------ the top of f16
@@ -84,13 +91,51 @@ def test_f16_decode_at_the_top_of_the_type(fia, n1, D, G, room):
     q = torch.randn(B, n1, 1, D, generator=g).half()
     q[0] = 0.0
     for lens in ([90, 1, 2], [77, 33, 16]):
-        out, lse, ref = attend(fia, q, p, table, lens, scale=D ** -0.5, room=room)
+        out, lse, ref, mid = attend(fia, q, p, table, lens, scale=D ** -0.5, room=room)
         assert out.isfinite().all()
-        io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D)
+        io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D, middle=mid)
     # keys as large: scores of their size, but for small queries
     p, table = written(fia, v, k, G, dt="f16")
-    out, lse, ref = attend(fia, (q.float() * 1e-5).half(), p, table, [90, 1, 17], scale=0.125, room=room)
-    io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D)
+    out, lse, ref, mid = attend(fia, (q.float() * 1e-5).half(), p, table, [90, 1, 17], scale=0.125, room=room)
+    io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D, middle=mid)
+
+
+# ------------------------------------------------------------------ the scores' factor
+ROWS = [(1, 64, 32, 0), (4, 128, 128, 0), (8, 128, 32, SHARED), (16, 128, 64, 0), (32, 64, 64, SHARED), (64, 64, 64, 0),
+        (48, 128, 128, SHARED), (64, 128, 32, 0)]    # rows of a unit, D, G, keys that the tables have room for
+
+
+@pytest.mark.parametrize("n1,D,G,room", ROWS)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [1e-9, 2.0 ** -60, 2.0 ** -126])
+def test_query_rows_of_zeros_and_small_scales(fia, n1, D, G, room, dt, scale):
+    """A row of zeros (a padded one) averages the values it sees, whatever the scale."""
+    g = torch.Generator().manual_seed(n1)
+    k, v = torch.randn(3, 90, 1, D, generator=g), torch.randn(3, 90, 1, D, generator=g) + 2
+    p, table = written(fia, k, v, G, dt=dt)
+    q = torch.randn(3, n1, 1, D, generator=g).to(DTYPES[dt])
+    q[0] = 0.0
+    q[:, ::3] = 0.0
+    q[:, 1::3] *= 2.0 ** -14
+    out, lse, ref, mid = attend(fia, q, p, table, [90, 1, 17], scale=scale, room=room)
+    assert out.isfinite().all()
+    io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D, middle=mid)
+
+
+@pytest.mark.parametrize("n1,D,G,room", ROWS)
+@pytest.mark.parametrize("at,scale", [(117, 0.125), (118, 0.125), (121, 0.125), (121, 2.0 ** 4), (-40, 2.0 ** 38), (-100, 2.0 ** 98),
+                                      (-120, 2.0 ** 118), (-126, 2.0 ** 120)])
+def test_queries_of_far_magnitudes(fia, n1, D, G, room, at, scale):
+    """bf16 queries of 2^at: scores of a few units all the same (the keys are rows of one value)."""
+    g = torch.Generator().manual_seed(n1 + at)
+    unit = 2.0 ** (-at) / (D * scale)
+    k = (torch.randn(3, 90, 1, 1, generator=g).double() * 3 * unit).expand(-1, -1, -1, D)
+    v = torch.randn(3, 90, 1, D, generator=g)
+    p, table = written(fia, k, v, G)
+    q = ((1 + torch.rand(3, n1, 1, D, generator=g).double()) * 2.0 ** at).bfloat16()
+    out, lse, ref, mid = attend(fia, q, p, table, [90, 1, 17], scale=scale, room=room)
+    assert np.isfinite(ref[1]).all() and ref[4].max() < 40
+    io.assert_close(out, lse, ref, 90, wide=n1 > 32 and G == D, middle=mid)
 
 
 # ------------------------------------------------------------------ work shared evenly among the CTAs
@@ -105,8 +150,8 @@ def test_shares_that_begin_with_any_sequence(fia, n1, Q, D, G):
     q = torch.randn(B, n1, Q, D, generator=g).bfloat16()
     for first, every in ((0, 1), (1, 7), (31, 33), (64, 2), (199, 1), (97, 50)):
         lens = [L - b % 9 if b >= first and (b - first) % every == 0 else 0 for b in range(B)]
-        out, lse, ref = attend(fia, q, p, table, lens, scale=D ** -0.5, room=SHARED)
-        io.assert_close(out, lse, ref, L, wide=n1 * Q > 32 and G == D)
+        out, lse, ref, mid = attend(fia, q, p, table, lens, scale=D ** -0.5, room=SHARED)
+        io.assert_close(out, lse, ref, L, wide=n1 * Q > 32 and G == D, middle=mid)
         wide = torch.nn.functional.pad(table, (0, SHARED // 16 - table.shape[1])).to(DEV)
         for _ in range(5):
             again = fia.fia_decode_window_int4(q.to(DEV), *p, actual_seq_kvlen=i32(lens), block_table=wide, block_size=16, num_heads=n1,
