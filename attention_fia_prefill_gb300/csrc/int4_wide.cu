@@ -13,9 +13,11 @@
 //   * A 16-byte piece of an operand's row is a word of codes: nibble i of its two
 //     units, i = 0..3.  Q is laid down in the same order, 16 times as large where it
 //     meets bits 0-3, and O's columns come out in it.
-//   * P' is at most 2^15: the maximum of S and the largest step of a step's keys bound
-//     it, lowered by 12, as a maximum is kept until it has grown by 3 (log2 units).  It
-//     is exact to 11 bits down to 2^-26 of the largest weight times the largest step.
+//   * P' is at most 2^15: the maximum is that of S_j + log2(step_j), lowered by 12, and
+//     kept until it has grown by 3 (log2 units).  Where every row sees every key and
+//     their steps are within 2^8 of each other, the largest S and the largest step bound
+//     it.  P' is exact to 11 bits down to 2^-26 (there 2^-18) of a row's largest weight
+//     times step, and a key that a row does not see has no part in it.
 //   * Even shares or clusters: as there, a step being a chunk.
 //   * A wait that runs out leaves NaN in the outputs of its unit and of those that
 //     the CTA would have come to.
@@ -66,7 +68,7 @@ struct WideCfg {
   static constexpr int kOffV = kOffK + kOperand;
   static constexpr int kOffRaw = kOffV + 2 * kOperand;
   static constexpr int kOffScale = kOffRaw + kTiles * kStages * kRaw;
-  static constexpr int kScale = 4 * kKeys * 4 + 16;   // of a step, fp32: K's step and low, V's; the tiles' log2(V's largest step) - 12
+  static constexpr int kScale = 4 * kKeys * 4 + 32;   // of a step, fp32: K's step and low, V's; the tiles' log2(V's largest, smallest step) - 12
   static constexpr int kScales = 4;                   // steps of them
   static constexpr int kOffRow = kOffScale + kScales * kScale; // sum of q and factor of each row
   static constexpr int kEnd = kOffRow + 2 * R * 4;
@@ -110,6 +112,9 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, wait(bar, parity, abort, limit_ns));
 }
+
+// log2 of a step of V, lowered by 12 (-42 at least: a page outside the pool has steps of 0).
+__device__ __forceinline__ float log2_step(float x) { return int4_detail::log2_approx(fmaf(x, 0x1p-12f, 0x1p-42f)); }
 
 // The 16 bytes of an operand that a word of codes makes.
 __device__ __forceinline__ uint4 spread(uint32_t w) {
@@ -386,9 +391,9 @@ __global__ void __launch_bounds__(kThreads, 2) int4_wide_kernel(const __grid_con
         const int j = tile_key(first_tile + i * stride + dw) + (lane & 15);
         const bool any = j < L && (j < p.sink || j >= sp.win);
         const float2 kk = int4_pair<BF16>(k2[0]), vv = int4_pair<BF16>(any ? v2[0] : 0u);
-        float most = vv.x;
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        // (as whole numbers: floats of 0 or more lie in the same order)
+        const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vv.x)));
+        const float least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(vv.x)));
         float* f = reinterpret_cast<float*>(smem + C::kOffScale + (it & 3) * C::kScale) + dw * kTile + lane;
         if (lane < kTile) {
           f[0] = kk.x * 0x1p20f;   // (products come in units of 2^-20)
@@ -396,7 +401,10 @@ __global__ void __launch_bounds__(kThreads, 2) int4_wide_kernel(const __grid_con
           f[2 * kKeys] = vv.x;
           f[3 * kKeys] = vv.y;
         }
-        if (lane == 0) f[4 * kKeys - dw * kTile + dw] = int4_detail::log2_approx(fmaf(most, 0x1p-12f, 0x1p-42f));
+        if (lane == 0) {
+          f[4 * kKeys - dw * kTile + dw] = log2_step(most);
+          f[4 * kKeys - dw * kTile + dw + 4] = log2_step(least);
+        }
       }
       warp_arrive(&bar->c_full[it & 3]);
       if (it >= 2 && !warp_wait(&bar->v_free[s], ((it >> 1) - 1) & 1, abort_flag, w.limit_ns)) break;
@@ -460,15 +468,24 @@ __global__ void __launch_bounds__(kThreads, 2) int4_wide_kernel(const __grid_con
         }
       }
       float top = -INFINITY;
+      const float4 a = *reinterpret_cast<const float4*>(sc + 4 * kKeys - g * C::kCols), z = *reinterpret_cast<const float4*>(sc + 4 * kKeys - g * C::kCols + 4);
+      const float most = fmax3(fmaxf(a.x, a.y), a.z, a.w);
+      if (full && most - fminf(fminf(z.x, z.y), fminf(z.z, z.w)) <= 8.f) {
 #pragma unroll
-      for (int c = 0; c < C::kCols / 2; ++c) {
-        float lo, hi;
-        f2_unpack(x[c], lo, hi);
-        top = fmax3(top, lo, hi);
-      }
-      {
-        const float4 a = *reinterpret_cast<const float4*>(sc + 4 * kKeys - g * C::kCols);
-        top = fmaf(top, cr, fmax3(fmaxf(a.x, a.y), a.z, a.w));
+        for (int c = 0; c < C::kCols / 2; ++c) {
+          float lo, hi;
+          f2_unpack(x[c], lo, hi);
+          top = fmax3(top, lo, hi);
+        }
+        top = fmaf(top, cr, most);
+      } else {
+#pragma unroll
+        for (int c = 0; c < C::kCols / 2; ++c) {
+          float lo, hi, st0, st1;
+          f2_unpack(x[c], lo, hi);
+          f2_unpack(*reinterpret_cast<const uint64_t*>(sc + 2 * kKeys + 2 * c), st0, st1);
+          top = fmax3(top, fmaf(lo, cr, log2_step(st0)), fmaf(hi, cr, log2_step(st1)));
+        }
       }
       const float m_use = (m == -INFINITY || top > m + 3.f) ? fmaxf(m, top) : m;
       const float alpha = m_use == m ? 1.f : fast_exp2(m - m_use);

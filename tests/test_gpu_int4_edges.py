@@ -157,3 +157,33 @@ def test_shares_that_begin_with_any_sequence(fia, n1, Q, D, G):
             again = fia.fia_decode_window_int4(q.to(DEV), *p, actual_seq_kvlen=i32(lens), block_table=wide, block_size=16, num_heads=n1,
                                                num_key_value_heads=1, scale_value=D ** -0.5, input_layout="BNSD")
             assert torch.equal(again[0], out)
+
+
+# ------------------------------------------------------------------ steps far above the others'
+@pytest.mark.parametrize("room", [0, SHARED])
+@pytest.mark.parametrize("n1,Q,D,dt", [(16, 4, 128, "bf16"), (9, 4, 64, "bf16"), (4, 16, 64, "bf16"), (16, 4, 128, "f16"), (4, 2, 64, "bf16"),
+                                       (8, 4, 128, "bf16")])
+@pytest.mark.parametrize("where", ["hidden", "light"])
+def test_values_far_above_the_others(fia, n1, Q, D, dt, room, where):
+    """A value row 2^40 times as wide as the others (f16: others 2^-9, it 2^14), that only the last token sees, or that
+    every token sees with a weight of about e^-60: the others' digits stay.
+
+    Weights times steps are rounded to 11 bits down to 2^-26 of their own largest, and to 2^-37 of it below; that is
+    assert_close with the row's own largest where it takes the sequence's."""
+    L = [61, 200]
+    g = torch.Generator().manual_seed(n1 + D)
+    k, v = (torch.randn(2, 200, 1, D, generator=g) for _ in range(2))
+    big = 2.0 ** 40
+    if dt == "f16":
+        v, big = v * 2.0 ** -9, 2.0 ** 23
+    q = torch.randn(2, n1, Q, D, generator=g)
+    for b, n in enumerate(L):
+        at = n - 1 if where == "hidden" else 20
+        v[b, at] *= big
+        if where == "light":
+            q[b, :, :, 0], k[b, :, 0, 0], k[b, at, 0, 0] = 12.0, 0.0, -50.0 * D ** 0.5 / 10
+    p, table = written(fia, k, v, D, dt=dt)
+    out, lse, ref, mid = attend(fia, q.to(DTYPES[dt]), p, table, L, scale=D ** -0.5, room=room)
+    ref = ref[:7] + (ref[6],)
+    pick = slice(0, Q - 1) if where == "hidden" else slice(0, Q)
+    io.assert_close(out[:, :, pick], lse[:, :, pick], tuple(x[:, :, pick] for x in ref), 200, wide=True, middle=None if mid is None else mid[:, :, pick])
