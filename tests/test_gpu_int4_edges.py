@@ -187,3 +187,83 @@ def test_values_far_above_the_others(fia, n1, Q, D, dt, room, where):
     ref = ref[:7] + (ref[6],)
     pick = slice(0, Q - 1) if where == "hidden" else slice(0, Q)
     io.assert_close(out[:, :, pick], lse[:, :, pick], tuple(x[:, :, pick] for x in ref), 200, wide=True, middle=None if mid is None else mid[:, :, pick])
+
+
+def shared_evenly(fia, q, p, **kw):
+    """Whether a call's work is shared evenly: then it needs a workspace, and refuses one of 256 bytes."""
+    try:
+        fia.fia_decode_window_int4(q, *p, workspace=torch.empty(256, dtype=torch.uint8, device=DEV), **kw)
+    except fia.FIAError as e:
+        assert "workspace" in str(e)
+        return True
+    return False
+
+
+@pytest.mark.parametrize("n1,n2,Q,D,G,dt", [(4, 2, 1, 64, 32, "f16"), (6, 1, 1, 128, 128, "bf16"), (8, 2, 3, 128, 32, "bf16"),
+                                            (10, 2, 5, 64, 64, "bf16"), (16, 2, 8, 128, 128, "bf16"), (16, 1, 4, 64, 64, "f16"),
+                                            (8, 1, 8, 128, 64, "bf16")])
+@pytest.mark.parametrize("pre,sink", [(1500, 20), (63, 300), (200, 0), (17, 5)])
+def test_windows_on_evenly_shared_work(fia, n1, n2, Q, D, G, dt, pre, sink):
+    """Windows that end in any chunk of a cut unit, gaps behind the sinks inside one; as many sequences as make the plan
+    one of shares.  A share of them is compared."""
+    bs, W = 16, 130
+    span = min(W * bs, pre + sink + Q)
+    rows = n1 // n2 * Q
+    B = min(-(-(33 * 152 * 16 if rows <= 8 else 33 * 152 * 8 if rows <= 16 else 33 * 152 * 4 if rows <= 32 else 33 * 152 * 2) // (n2 * (span // 16))),
+            100000)
+    r = np.random.default_rng(pre + n1)
+    lens = np.where(r.random(B) < min(0.5, 400 / B), r.integers(0, W * bs + 1, B), r.integers(0, 60, B))
+    g = torch.Generator().manual_seed(pre + D)
+    blocks = 400
+    p, _ = written(fia, *(torch.randn(blocks, bs, n2, D, generator=g) for _ in range(2)), G, dt=dt)
+    table = r.integers(0, blocks, (B, W)).astype(np.int32)
+    q = torch.randn(B, n1, Q, D, generator=g).to(DTYPES[dt])
+    kw = dict(actual_seq_kvlen=i32(lens.tolist()), block_table=torch.from_numpy(table).to(DEV), block_size=bs, num_heads=n1,
+              num_key_value_heads=n2, scale_value=D ** -0.5, input_layout="BNSD", pre_tokens=pre, sink_tokens=sink, softmax_lse_flag=True)
+    assert shared_evenly(fia, q.to(DEV), p, **kw)
+    out, lse = fia.fia_decode_window_int4(q.to(DEV), *p, **kw)
+    long = np.flatnonzero(lens >= 60)
+    pick = np.concatenate([np.arange(10), r.choice(long, min(25, len(long)), False), r.integers(0, B, 15), np.arange(B - 5, B)])
+    parts = [io.pool_parts(p[0], p[2]), io.pool_parts(p[1], p[3])]
+    rows_ = [[io.rows(x, table[b], lens[b]) for b in pick] for x in parts]
+    ref = io.decode(q[pick], *rows_, lens[pick], pre, sink, D ** -0.5)
+    middle = None
+    if dt == "f16":
+        steps = np.repeat(f64(p[3]).transpose(0, 2, 1, 3, 4)[..., 0], G, -1)
+        middle = io.middles(q[pick], *rows_, [io.rows((steps,), table[b], lens[b])[0] for b in pick], lens[pick], pre, sink, D ** -0.5)
+    io.assert_close(out[pick], lse[pick], ref, W * bs, wide=rows > 32 and G == D, middle=middle)
+    # and all of them against calls of a few sequences each, which clusters of CTAs take
+    worst = 0.0
+    for a in range(0, B, 96):
+        few = dict(kw, actual_seq_kvlen=kw["actual_seq_kvlen"][a:a + 96], block_table=kw["block_table"][a:a + 96])
+        some = fia.fia_decode_window_int4(q[a:a + 96].to(DEV), *p, **few)[0]
+        worst = max(worst, (some.float() - out[a:a + 96].float()).abs().max().item())
+    # (two results of averages of values below 8: their roundings, and those of P in 11 bits, twice)
+    assert f64(p[3])[..., 1].min() > -8 and worst <= 2 * 8 * (torch.finfo(DTYPES[dt]).eps / 2 + 2.0 ** -10)
+
+
+@pytest.mark.parametrize("n1,Q,D,G", [(10, 4, 64, 64), (16, 4, 128, 128), (4, 4, 64, 32), (2, 4, 128, 128)])
+@pytest.mark.parametrize("at,pre", [(59, 200), (58, 200), (40, 18)])
+@pytest.mark.parametrize("which", [0, 1])
+def test_nan_keys_on_evenly_shared_work(fia, n1, Q, D, G, at, pre, which):
+    """A NaN key or value reaches the tokens that see it, and no other: of its sequence, and of those behind it in a share."""
+    bs, L, W = 16, 61, 16
+    x = [torch.randn(1, 64, 1, D, generator=torch.Generator().manual_seed(i)) for i in (1, 2)]
+    x[which][0, at, 0, 7] = float("nan")
+    p, _ = written(fia, *x, G)
+    B = 33 * 152 * (16 if n1 * Q <= 8 else 8 if n1 * Q <= 16 else 2) // (min(W * bs, pre + Q) // 16) + 1
+    q = torch.randn(1, n1, Q, D, generator=torch.Generator().manual_seed(3)).bfloat16().expand(B, -1, -1, -1).contiguous()
+    lens = torch.where(torch.arange(B) % 3 == 0, L, torch.arange(B) % 24).to(torch.int32).to(DEV)
+    table = torch.arange(W, dtype=torch.int32).clamp(max=3).expand(B, W).contiguous().to(DEV)
+    kw = dict(actual_seq_kvlen=lens, block_table=table, block_size=bs, num_heads=n1, num_key_value_heads=1, scale_value=0.1,
+              input_layout="BNSD", pre_tokens=pre, softmax_lse_flag=True)
+    assert shared_evenly(fia, q.to(DEV), p, **kw)
+    out, lse = fia.fia_decode_window_int4(q.to(DEV), *p, **kw)
+    i = np.arange(L - Q, L)
+    see = torch.from_numpy((at <= i) & (at >= i - pre))
+    assert see.any() and not see.all()
+    group = slice(7 // G * G, 7 // G * G + G) if which else slice(0, D)
+    bad = torch.zeros(n1, Q, D, dtype=torch.bool)
+    bad[:, see, group] = True
+    nan = out.isnan().cpu()
+    assert (nan[::3] == bad).all() and not nan[1::3].any() and not nan[2::3].any()
