@@ -267,3 +267,19 @@ def test_nan_keys_on_evenly_shared_work(fia, n1, Q, D, G, at, pre, which):
     bad[:, see, group] = True
     nan = out.isnan().cpu()
     assert (nan[::3] == bad).all() and not nan[1::3].any() and not nan[2::3].any()
+
+
+def test_a_call_that_needs_a_workspace_records_no_error(fia):
+    """The binding makes the workspace of a call with much work, and the last error stays that of the last call that failed."""
+    from attention_fia_prefill_gb300 import _binding as B
+    lib = B.load_library()
+    g = torch.Generator().manual_seed(1)
+    p, table = written(fia, *(torch.randn(2, 40, 1, 64, generator=g) for _ in range(2)), 64)
+    q = torch.randn(2, 4, 1, 64, generator=g).bfloat16()
+    with pytest.raises(fia.FIAError, match="in blocks of 16"):
+        fia.fia_decode_window_int4(q.to(DEV), *p, actual_seq_kvlen=i32([1, 1]), block_table=table.to(DEV), block_size=-3, num_heads=4,
+                                   num_key_value_heads=1, input_layout="BNSD")
+    said = lib.fia_last_error()
+    for room in (0, SHARED):
+        attend(fia, q, p, table, [40, 3], room=room)
+        assert lib.fia_last_error() == said
