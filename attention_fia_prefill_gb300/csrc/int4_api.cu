@@ -122,9 +122,9 @@ struct SplitPlan {
 
 // A unit to a cluster leaves SMs to wait for the longest one; even shares need a
 // scan of the lengths first and a second kernel, which joins what they cut.  (us, clusters
-// and shares, by the tiles that a group has with all keys: 4 13.4 21.5; 13 16.5 17.2; 27
-// 20.9 22.6; 54, equal lengths, 73 72; 108, equal lengths, 94 95; 215, lengths of 1 to 80,
-// 124 94; 431, 1 to 36, 230 210.)
+// and shares, by the tiles that a group has with all keys, tables as wide as the longest
+// sequence: 4 13.4 21.5; 13 16.5 17.2; 27 20.9 22.6; 54, equal lengths, 73 72; 108, equal
+// lengths, 94 95; 215, lengths of 1 to 80, 124 94; 431, 1 to 36, 230 210.)
 SplitPlan split_plan(const SpanParams& p, const Int4Pool& o, int n_sm) {
   constexpr int64_t kLeast = 32;   // tiles of 16 keys for a group of warps, with all keys that the tables hold
   const Int4Shape c = int4_shape(p.rows, int(o.groups));

@@ -41,10 +41,11 @@
 //     joined across lanes only in steps that raise one.
 // 33 rows and more in one group a row: int4_wide.cu.
 // Bound: HBM for units of up to 8 rows and long contexts (64 sequences of up to 32768
-// keys, 8 heads: 188 us, 6.2 TB/s, 92% of a copy's rate); a warp's chain load -> product
+// keys, 8 heads: 189 us, 6.2 TB/s, 92% of a copy's rate); a warp's chain load -> product
 // -> softmax -> product elsewhere: 16 rows a unit 87 us where HBM would take 43 (64 x 4
-// tokens, window 4096; 359 instructions a tile at 1.9 a cycle with 8 warps an SM; 12
-// warps of fewer registers take as long), 16 sequences of up to 4096 keys 16.5 us, one of
+// tokens, window 4096; 349 instructions a tile at 1.9 a cycle with 8 warps an SM; 12
+// warps of fewer registers take as long), 32 rows 153 where it would take 45 (32 sequences of
+// up to 16384 keys; 562 instructions a tile at 1.8 a cycle), 16 sequences of up to 4096 keys 16.5 us, one of
 // 20001 12.8 us (start 3, first keys 1.2, ten steps of 0.8, join 2).  Tried for the last:
 // a ring of 8 steps 19.4 us (clusters of 16 CTAs then wait for 16 free SMs), of 5 steps
 // 12.8, 8 warps a CTA 12.9.  Joining a unit's parts in the CTA that writes the last one
@@ -67,6 +68,11 @@ constexpr int kTile = 16;
 template <int D, int NG, int NT, int MT>
 struct Cfg {
   static constexpr int kWarps = 4;
+  // CTAs that registers allow an SM, and the clusters' plan counts.  With a cluster's part of shared memory three fit at head
+  // dim 128 for 5 to 8 rows, and for fewer in groups of 32 and 64.  Of 224 calls (7 to 72 sequences of 8 heads, up to 512 or 2048
+  // keys), in the mean and singly: three counted 0.98 (0.66 to 1.47: 16 sequences of up to 512 keys 10.1 -> 7.0 us, 60 10.5 ->
+  // 15.5); the part laid in the rings, so that four fit, and no dearer cluster taken where three do 0.93 (0.68 to 1.28: 56
+  // sequences of 512 keys, 8 rows, 9.1 -> 11.1, as they no longer spread three an SM).
   static constexpr int kResident = NT <= 1 ? 4 : 2;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kGroups = kWarps / MT;
@@ -89,7 +95,7 @@ struct Cfg {
   static constexpr int kSmem = kOffQ + kQ + 128;
   // even shares: nothing comes from other CTAs
   static constexpr int kOffQShare = kOffIn, kSmemShare = kOffQShare + kQ + 128;
-  static_assert(int4_shape(kRows, NG).resident * (kSmemShare + 128 + 1024) <= 228 * 1024, "as many CTAs as an SM is counted for");
+  static_assert(int4_shape(kRows, NG).resident * (kSmemShare + 128 + 1024) <= 228 * 1024, "as many CTAs of shares as an SM is counted for");
 };
 
 // Row of a fragment's index -> key of the tile: a lane pair's keys 2t and 2t + 1
@@ -1062,7 +1068,9 @@ cudaError_t launch_one(Int4SpanParams p, int n_sm, cudaStream_t s) {
     if (e == cudaSuccess) e = launch_early(kernel, dim3(unsigned(p.s.N2), unsigned(p.n_ctas / p.s.N2)), C::kThreads, C::kSmemShare, s, p);
     return e == cudaSuccess ? launch_join<D, BF16>(p, s) : e;
   }
-  constexpr int kStart = 4;   // start cost of a CTA in tiles
+  // start cost of a CTA in tiles: 0, 2, 8 of them take 1.20, 1.02, 0.99 times as long in the mean of 196 calls (1 to 64
+  // sequences of 8 heads, 4 to 32 rows, up to 16000 keys), and 8 up to 1.09 times (20 of up to 4000 keys 22.7 -> 24.7 us)
+  constexpr int kStart = 4;
   const int64_t span = std::min<int64_t>(p.s.kv_max, int64_t(p.s.sink) + p.s.pre + p.s.q_tokens);
   int cs = cluster_ctas(int64_t(p.s.B) * p.s.N2, p.s.rows, span / kTile + 1, C::kGroups, kStart, span < p.s.kv_max,
                         C::kResident, n_sm);

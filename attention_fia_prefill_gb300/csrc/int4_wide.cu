@@ -21,12 +21,14 @@
 //   * Even shares or clusters: as there, a step being a chunk.
 //   * A wait that runs out leaves NaN in the outputs of its unit and of those that
 //     the CTA would have come to.
-// In us, here and with mma.sync (and at HBM's rate), 8 heads of 64 rows: 16 sequences of 100 to
-// 8192 keys 59, 87 (11); 32 of up to 16384 185, 255 (46); 8 of up to 1024 21, 21; one of
-// 500 15, 13.  With 32 rows in four copies 173 where mma.sync takes 154 (32 of up to
+// In us, here and with mma.sync (and at HBM's rate), 8 heads of 64 rows, caches not in L2: 16
+// sequences of 100 to 8192 keys 62, 82 (11); 32 of up to 16384 177, 257 (46); 8 of up to 1024
+// 20, 21; one of 500 15, 13.  With 32 rows in four copies 173 where mma.sync takes 154 (32 of up to
 // 16384), so units of up to 32 rows are left to that.
-// Bound: shared memory's data path.  A step of 64 keys is 1500 cycles, of which the
-// products read Q, K and V for 505 and loads, stores and the scales' broadcasts take 960.
+// Bound: shared memory's data path.  A step of 64 keys is 1370 cycles, of which the
+// products read Q, K and V for 490 and loads, stores and the scales' broadcasts take 925.
+// The steps' largest and smallest by redux instead of shuffles: 181 -> 176 us (32 of up to
+// 16384); the branch between the two maxima costs f16 at head dim 64 2.5% (153 -> 157).
 // K and V unpacked by four warps each were slower (184 -> 217 us), K twice and V once too
 // (174 -> 233).
 #include <algorithm>
@@ -633,7 +635,9 @@ cudaError_t launch_one(Int4WideParams w, int n_sm, cudaStream_t s) {
     return e == cudaSuccess ? int4_detail::launch_join<D, BF16>(w.i, s) : e;
   }
   constexpr auto kernel = int4_wide_kernel<D, BF16, false>;
-  constexpr int kStart = 10;         // start cost of a CTA in steps
+  constexpr int kStart = 10;         // start cost of a CTA in steps (2, 5 and 20: each of 98 calls within 5%)
+  // (always for units of like lengths: a dearer cluster, to even lengths out, takes 1.01 times as long in the mean of 98 calls
+  // of 1 to 64 sequences, and up to 1.30 times: 4 of 64 keys 9.0 -> 11.7 us)
   const int64_t span = std::min<int64_t>(ip.s.kv_max, int64_t(ip.s.sink) + ip.s.pre + ip.s.q_tokens);
   set_span_shape(w.i.s, cluster_ctas(int64_t(ip.s.B) * ip.s.N2, ip.s.rows, span / kKeys + 1, 1, kStart, true, 2, n_sm));
   cudaError_t e = prepare_span<kernel>(smem);
